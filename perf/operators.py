@@ -3,8 +3,8 @@ attention that reads it, and evicting tokens from it by the attention weight the
 
 The cache holds K and V rows as E4M3 codes [batch, T, G, d] with one power-of-two scale for every
 block of `block` tokens and KV group, [batch, ceil(T / block), G]: s = 2^e, e the smallest integer
->= -126 with max |x| <= 448 s over the block's finite values; a code is x / s rounded to nearest even,
-saturating, NaN kept.
+of [-126, 119] with max |x| <= 448 s over the block's finite values (119: code times scale stays
+finite); a code is x / s rounded to nearest even, saturating, NaN kept.
 
   append   tokens lens[b] .. lens[b] + counts[b] - 1 of every sequence join the cache; the scale of a
            block that holds tokens already grows with the new ones where it has to, and the codes that
@@ -176,7 +176,7 @@ def _exponent(amax):
     """e of the scale from a block's largest magnitude: amax = m 2^E, m in [1/2, 1), 448 = 7/8 2^9."""
     m, E = torch.frexp(amax)
     e = E - 9 + (m > 0.875).to(E.dtype)
-    return torch.where(amax > 0, e, -126).clamp(min=-126)
+    return torch.where(amax > 0, e, -126).clamp(-126, 119)
 
 
 def _values(codes, scale, block):
@@ -334,11 +334,11 @@ def _grid(y):
 
 
 def _scale64(amax):
-    """The smallest power of two, at least 2^-126, whose 448-fold reaches amax."""
+    """The smallest power of two from 2^-126 to 2^119 whose 448-fold reaches amax."""
     e = torch.ceil(torch.log2(torch.where(amax > 0, amax, E4M3_MAX) / E4M3_MAX))
     sc = torch.exp2(e)
     sc = torch.where(sc * E4M3_MAX < amax, sc * 2, torch.where(sc / 2 * E4M3_MAX >= amax, sc / 2, sc))
-    return torch.where(amax > 0, sc, 0.0).clamp(min=2.0 ** -126)
+    return torch.where(amax > 0, sc, 0.0).clamp(2.0 ** -126, 2.0 ** 119)
 
 
 def _rows64(codes, scale, rows, g, block):
