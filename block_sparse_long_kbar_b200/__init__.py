@@ -29,7 +29,8 @@ EXPORTS = ["sgqa_status_string", "sgqa_version", "sgqa_workspace_size", "sgqa_de
            "sgqa_reset_device_status", "sgqa_get_device_status", "sgqa_compress_keys", "sgqa_select",
            "sgqa_attend", "sgqa_forward", "sgqa_decode", "sgqa_decode_noalloc", "sgqa_gated_swa",
            "sgqa_quantize_kv_fp8", "sgqa_decode_fp8", "sgqa_test_stall_decode_cta", "sgqa_forward_rows",
-           "sgqa_backward_workspace_size", "sgqa_attend_backward"]
+           "sgqa_backward_workspace_size", "sgqa_attend_backward", "sgqa_cache8_workspace_size", "sgqa_cache8_append",
+           "sgqa_cache8_attend", "sgqa_cache8_evict"]
 
 
 class SgqaError(RuntimeError):
@@ -84,9 +85,15 @@ def load_library():
     L.sgqa_backward_workspace_size.restype = S
     L.sgqa_backward_workspace_size.argtypes = [D]
     L.sgqa_attend_backward.argtypes = [D] + [P] * 11 + [S, P]
+    L.sgqa_cache8_workspace_size.restype = S
+    L.sgqa_cache8_workspace_size.argtypes = [D, I, I]
+    L.sgqa_cache8_append.argtypes = [D, I, P, P, I] + [P] * 7 + [S, P]
+    L.sgqa_cache8_attend.argtypes = [D, I, P, I] + [P] * 10 + [S, P]
+    L.sgqa_cache8_evict.argtypes = [D, I, P, I, I, I] + [P] * 13 + [S, P]
     for n in ("sgqa_reset_device_status", "sgqa_get_device_status", "sgqa_compress_keys", "sgqa_select",
               "sgqa_attend", "sgqa_forward", "sgqa_decode", "sgqa_decode_noalloc", "sgqa_gated_swa",
-              "sgqa_quantize_kv_fp8", "sgqa_decode_fp8", "sgqa_test_stall_decode_cta", "sgqa_forward_rows", "sgqa_attend_backward"):
+              "sgqa_quantize_kv_fp8", "sgqa_decode_fp8", "sgqa_test_stall_decode_cta", "sgqa_forward_rows", "sgqa_attend_backward",
+              "sgqa_cache8_append", "sgqa_cache8_attend", "sgqa_cache8_evict"):
         getattr(L, n).restype = I
     _lib = L
     return L
@@ -271,6 +278,40 @@ def sgqa_decode_fp8(dims, cache_len, n_new, k8_cache, k_scale, v8_cache, v_scale
         _ptr(kbar_cache, "kbar_cache"), _ptr(q_new, "q_new"), _ptr(k_new, "k_new"), _ptr(v_new, "v_new"),
         _ptr(qidx_new, "qidx_new"), _ptr(kidx_new, "kidx_new"), _ptr(gate_new, "gate_new"), _ptr(out, "out"),
         _ptr(sel_out, "sel_out"), _ptr(ws, "ws"), ws.numel(), _stream(stream)))
+
+
+def sgqa_cache8_workspace_size(dims: sgqa_dims, block: int, n_new: int) -> int:
+    return int(load_library().sgqa_cache8_workspace_size(ctypes.byref(dims), int(block), int(n_new)))
+
+
+def sgqa_cache8_append(dims, block, lens, n_t, k_new, v_new, k8, k_scale, v8, v_scale, ws, counts=None, stream=None):
+    """Store the first counts[b] (default: all n_t) tokens of k_new, v_new behind the lens[b] cached ones."""
+    _check("sgqa_cache8_append", load_library().sgqa_cache8_append(
+        ctypes.byref(dims), int(block), _ptr(lens, "lens"), _ptr(counts, "counts"), int(n_t), _ptr(k_new, "k_new"),
+        _ptr(v_new, "v_new"), _ptr(k8, "k8"), _ptr(k_scale, "k_scale"), _ptr(v8, "v8"), _ptr(v_scale, "v_scale"),
+        _ptr(ws, "ws"), ws.numel(), _stream(stream)))
+
+
+def sgqa_cache8_attend(dims, block, lens, n_new, q, gate, k8, k_scale, v8, v_scale, out, ws, weight_in=None,
+                       weight_out=None, stream=None):
+    """Dense gated attention of the last n_new of lens[b] tokens over the block-scaled 8-bit cache; with
+    weight_out, also the attention weight that every token has received (on top of weight_in)."""
+    _check("sgqa_cache8_attend", load_library().sgqa_cache8_attend(
+        ctypes.byref(dims), int(block), _ptr(lens, "lens"), int(n_new), _ptr(q, "q"), _ptr(gate, "gate"),
+        _ptr(k8, "k8"), _ptr(k_scale, "k_scale"), _ptr(v8, "v8"), _ptr(v_scale, "v_scale"), _ptr(out, "out"),
+        _ptr(weight_in, "weight_in"), _ptr(weight_out, "weight_out"), _ptr(ws, "ws"), ws.numel(), _stream(stream)))
+
+
+def sgqa_cache8_evict(dims, block, lens, keep, recent, T_out, weight, k8, k_scale, v8, v_scale, k8_out, k_scale_out,
+                      v8_out, v_scale_out, weight_out, kept, lens_out, ws, stream=None):
+    """Move the `recent` last and the heaviest other tokens, `keep` in all per (sequence, group), to
+    another cache of capacity T_out."""
+    _check("sgqa_cache8_evict", load_library().sgqa_cache8_evict(
+        ctypes.byref(dims), int(block), _ptr(lens, "lens"), int(keep), int(recent), int(T_out),
+        _ptr(weight, "weight"), _ptr(k8, "k8"), _ptr(k_scale, "k_scale"), _ptr(v8, "v8"), _ptr(v_scale, "v_scale"),
+        _ptr(k8_out, "k8_out"), _ptr(k_scale_out, "k_scale_out"), _ptr(v8_out, "v8_out"),
+        _ptr(v_scale_out, "v_scale_out"), _ptr(weight_out, "weight_out"), _ptr(kept, "kept"),
+        _ptr(lens_out, "lens_out"), _ptr(ws, "ws"), ws.numel(), _stream(stream)))
 
 
 def sgqa_test_stall_decode_cta(cta: int):

@@ -1,0 +1,165 @@
+// Appending tokens to the block-scaled 8-bit KV cache (format: cache8.cuh).
+//
+// A work item is one touched block of one (sequence, group), K and V together: every thread loads
+// 16 dims of a row (two 16-byte loads of bf16 for K, two for V), the item's largest finite
+// magnitudes meet in shared memory, and the codes go out as one 16-byte store per row piece: each
+// new element is read once and written once, no second pass. A block that held tokens before keeps
+// its scale unless a new token needs a larger one; only then are its codes read, rounded again and
+// rewritten. HBM bound: 2 bytes read and 1 written per element.
+#include "cache8.cuh"
+
+namespace sgqa {
+namespace {
+
+constexpr int kThr = 256;
+
+// Largest finite magnitude (bf16 bits) of eight bf16 values.
+__device__ __forceinline__ uint32_t amax8(const uint4& x) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
+    if (lo < 0x7F80u) m = max(m, lo);
+    if (hi < 0x7F80u) m = max(m, hi);
+  }
+  return m;
+}
+__device__ __forceinline__ uint2 encode8(const uint4& x, float inv) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] = c8_encode2(bf16_lo(w[i]) * inv, bf16_hi(w[i]) * inv);
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+// D: head dim; BLK: tokens per block. Rows of a block are spread over the threads, D / 16 to a row;
+// small blocks share a CTA (a warp always serves one item), large ones take several passes.
+template <int D, int BLK>
+__global__ void __launch_bounds__(kThr) cache8_append_kernel(C8AppendArgs a, int blocks_per_seq) {
+  constexpr int kTpr = D / 16, kRows = kThr / kTpr;
+  constexpr int kItems = kRows > BLK ? kRows / BLK : 1;
+  constexpr int kPass = BLK > kRows ? BLK / kRows : 1;
+  __shared__ uint32_t amax[kItems][2];
+  const int tid = threadIdx.x;
+  if (tid < kItems * 2) amax[tid / 2][tid & 1] = 0u;
+  __syncthreads();
+  const int sub = kItems > 1 ? (tid / kTpr) / BLK : 0;
+  const int row0 = kItems > 1 ? (tid / kTpr) % BLK : tid / kTpr;
+  const int col = (tid % kTpr) * 16;
+  const long item = (long)blockIdx.x * kItems + sub;  // (b, touched block, g), g fastest
+  const long per_seq = (long)blocks_per_seq * a.G;
+  const int b = (int)(item / per_seq);
+  const int g = (int)(item % a.G);
+  bool live = b < a.batch;
+  int L = 0, end = 0, j = 0;
+  if (live) {
+    const int cnt = a.counts ? __ldg(a.counts + b) : a.n_t;
+    L = __ldg(a.lens + b);
+    live = L >= 0 && cnt >= 0 && cnt <= a.n_t && (long)L + cnt <= a.T;
+    if (!live) report(a.status, SGQA_ERR_DEVICE_CHECK);
+    end = L + cnt;
+    j = L / BLK + (int)((item % per_seq) / a.G);
+    live = live && cnt > 0 && (long)j * BLK < end;
+  }
+  uint4 xk[kPass][2], xv[kPass][2];
+  uint32_t mk = 0, mv = 0;
+  const long u0 = (long)j * BLK;
+#pragma unroll
+  for (int p = 0; p < kPass; ++p) {
+    const long u = u0 + row0 + p * kRows;
+    xk[p][0] = xk[p][1] = xv[p][0] = xv[p][1] = make_uint4(0, 0, 0, 0);
+    if (live && u >= L && u < end) {
+      const long src = (((long)b * a.n_t + (u - L)) * a.G + g) * D + col;
+      const uint4* pk = reinterpret_cast<const uint4*>(a.k + src);
+      const uint4* pv = reinterpret_cast<const uint4*>(a.v + src);
+      xk[p][0] = __ldg(pk);
+      xk[p][1] = __ldg(pk + 1);
+      xv[p][0] = __ldg(pv);
+      xv[p][1] = __ldg(pv + 1);
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < kPass; ++p) {
+    mk = max(mk, max(amax8(xk[p][0]), amax8(xk[p][1])));
+    mv = max(mv, max(amax8(xv[p][0]), amax8(xv[p][1])));
+  }
+  mk = __reduce_max_sync(0xFFFFFFFFu, mk);
+  mv = __reduce_max_sync(0xFFFFFFFFu, mv);
+  if ((tid & 31) == 0) {
+    atomicMax(&amax[sub][0], mk);
+    atomicMax(&amax[sub][1], mv);
+  }
+  // the scales of a block that holds tokens already (read by all before one thread writes them)
+  const long nblk = (a.T + BLK - 1) / BLK;
+  const long si = ((long)b * nblk + j) * a.G + g;
+  const bool held = live && u0 < L;
+  const int ek_old = held ? c8_scale_exponent(a.c.ks[si]) : -126;
+  const int ev_old = held ? c8_scale_exponent(a.c.vs[si]) : -126;
+  __syncthreads();
+  if (!live) return;
+  const int ek = max(ek_old, c8_exponent(amax[sub][0] << 16)), ev = max(ev_old, c8_exponent(amax[sub][1] << 16));
+  const float ik = c8_pow2(-ek), iv = c8_pow2(-ev);
+#pragma unroll
+  for (int p = 0; p < kPass; ++p) {
+    const long u = u0 + row0 + p * kRows;
+    if (u >= end) break;
+    const long dst = (((long)b * a.T + u) * a.G + g) * D + col;
+    uint4* ok = reinterpret_cast<uint4*>(a.c.k8 + dst);
+    uint4* ov = reinterpret_cast<uint4*>(a.c.v8 + dst);
+    if (u >= L) {
+      const uint2 k0 = encode8(xk[p][0], ik), k1 = encode8(xk[p][1], ik);
+      const uint2 v0 = encode8(xv[p][0], iv), v1 = encode8(xv[p][1], iv);
+      *ok = make_uint4(k0.x, k0.y, k1.x, k1.y);
+      *ov = make_uint4(v0.x, v0.y, v1.x, v1.y);
+    } else {
+      if (ek > ek_old) {
+        const float f = c8_shift(ek_old - ek);
+        const uint4 w = *ok;
+        *ok = make_uint4(c8_rescale4(w.x, f), c8_rescale4(w.y, f), c8_rescale4(w.z, f), c8_rescale4(w.w, f));
+      }
+      if (ev > ev_old) {
+        const float f = c8_shift(ev_old - ev);
+        const uint4 w = *ov;
+        *ov = make_uint4(c8_rescale4(w.x, f), c8_rescale4(w.y, f), c8_rescale4(w.z, f), c8_rescale4(w.w, f));
+      }
+    }
+  }
+  if (row0 == 0 && col == 0) {
+    a.c.ks[si] = c8_pow2(ek);
+    a.c.vs[si] = c8_pow2(ev);
+  }
+}
+
+template <int D, int BLK>
+cudaError_t launch(const C8AppendArgs& a, cudaStream_t s) {
+  constexpr int kRows = kThr / (D / 16);
+  constexpr int kItems = kRows > BLK ? kRows / BLK : 1;
+  // n_t tokens can touch one block more than they fill, but never more than there are
+  const long nblk = ((long)a.T + BLK - 1) / BLK;
+  const long touched = ((long)a.n_t + BLK - 1) / BLK + 1;
+  const int per_seq = (int)(touched < nblk ? touched : nblk);
+  const long items = (long)a.batch * per_seq * a.G;
+  const long ctas = (items + kItems - 1) / kItems;
+  if (ctas > 0x7FFFFFFFL) return cudaErrorInvalidConfiguration;
+  cache8_append_kernel<D, BLK><<<(unsigned)ctas, kThr, 0, s>>>(a, per_seq);
+  return cudaGetLastError();
+}
+template <int D>
+cudaError_t launch_d(const C8AppendArgs& a, cudaStream_t s) {
+  switch (a.block) {
+    case 8: return launch<D, 8>(a, s);
+    case 16: return launch<D, 16>(a, s);
+    case 32: return launch<D, 32>(a, s);
+    case 64: return launch<D, 64>(a, s);
+    default: return launch<D, 128>(a, s);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_cache8_append(const C8AppendArgs& a, cudaStream_t s) {
+  return a.d == 64 ? launch_d<64>(a, s) : launch_d<128>(a, s);
+}
+
+}  // namespace sgqa

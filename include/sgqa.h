@@ -224,6 +224,69 @@ int sgqa_gated_swa(const sgqa_dims* dims, int window, const uint16_t* q, const u
                    const uint16_t* v, const uint16_t* gate, uint16_t* out, int32_t* sel_out,
                    void* ws, size_t ws_bytes, void* stream);
 
+/* The block-scaled 8-bit KV cache: K and V rows as FP8 E4M3 codes with one scale per block of tokens
+ * and KV group, for sequences of their own lengths. No counterpart on the pages beyond their statement
+ * that the KV cache is trained for FP8 storage (as sgqa_quantize_kv_fp8); the dense layer is their
+ * Gated GQA (mo.ai.kr, "Step 5 Preview agentic work design", section "model structure and training
+ * stability": Sparse GQA sits on top of Gated GQA).
+ *   k8, v8            [batch, T, G, d] uint8 codes, dims->T = capacity
+ *   k_scale, v_scale  [batch, ceil(T / block), G] fp32 powers of two
+ *   lens              [batch] int32 on the DEVICE: tokens that each sequence holds, 0 .. T
+ * block is 8, 16, 32, 64 or 128 tokens. The scale of a block is s = 2^e, e the smallest integer of
+ * [-126, 119] with max |x| <= 448 s over the finite values of its tokens; a code is x / s rounded to
+ * the nearest E4M3 value (ties to even), magnitudes above 448 s and infinities saturate, NaN stays
+ * NaN. code * s is exact in bf16. What lies behind a sequence's last token (codes, scales of blocks
+ * without tokens, weights) is never read into a result and never written.
+ * The lengths are read on the device when the call runs, so that one captured graph serves every
+ * length. One that does not fit (negative, or beyond the capacity) is recorded as
+ * SGQA_ERR_DEVICE_CHECK and its sequence is skipped (append) or taken as empty (attend, evict).
+ * Of dims, d_idx, B and k are checked like everywhere but not used.
+ *
+ * Bytes of workspace that any of the three calls below needs, n_new being the most tokens a step of
+ * sgqa_cache8_attend has; 0 if invalid or unsupported. */
+size_t sgqa_cache8_workspace_size(const sgqa_dims* dims, int block, int n_new);
+
+/* Appends tokens: of k_new, v_new [batch, n_t, G, d] bf16 the first counts[b] rows (counts [batch]
+ * int32 on the device, 0 .. n_t; NULL: all n_t) are stored at positions lens[b] .. lens[b] + counts[b]
+ * - 1. lens is not changed: the caller adds the counts to it. The scale of a block that holds tokens
+ * already is the larger of its own and the one the new tokens need; where it grows, the codes that
+ * the block holds are rounded again to the new one. So a cache filled in pieces can differ from one
+ * filled at once in such codes (by at most half a step of the grown scale), and repeating an append
+ * gives the same bits. n_t >= 0; lens[b] + counts[b] <= T. */
+int sgqa_cache8_append(const sgqa_dims* dims, int block, const int32_t* lens, const int32_t* counts, int n_t,
+                       const uint16_t* k_new, const uint16_t* v_new, uint8_t* k8, float* k_scale, uint8_t* v8,
+                       float* v_scale, void* ws, size_t ws_bytes, void* stream);
+
+/* Dense gated attention of the last n_new of each sequence's lens[b] tokens (appended before) over the
+ * whole cache: with p_i = lens[b] - n_new + i the position of query i, head h of group g and x = code *
+ * scale,  o = softmax_{u <= p_i}(q[b,i,h] . k[b,u,g] / sqrt(d)) v;  out[b,i,h,:] = o *
+ * sigmoid(gate[b,i,h,:]).  q, gate, out [batch, n_new, Hq, d] bf16. Rows without a position (p_i < 0)
+ * get zeros.
+ * weight_out, if not NULL, [batch, G, T] fp32, receives for every token u < lens[b]
+ *   (u < lens[b] - n_new ? weight_in[b,g,u] : 0) + sum over i and the heads of g of its probability,
+ * the attention weight it has received so far, when weight_in [batch, G, T] is what the step before
+ * wrote (NULL: nothing yet; it may be weight_out itself).
+ * Requires n_new * Hq/G <= 64 (else SGQA_ERR_UNSUPPORTED). */
+int sgqa_cache8_attend(const sgqa_dims* dims, int block, const int32_t* lens, int n_new, const uint16_t* q,
+                       const uint16_t* gate, const uint8_t* k8, const float* k_scale, const uint8_t* v8,
+                       const float* v_scale, uint16_t* out, const float* weight_in, float* weight_out, void* ws,
+                       size_t ws_bytes, void* stream);
+
+/* Evicts tokens: of each (sequence, group) at most `keep` stay and move, in order of position, to
+ * another cache of capacity T_out >= keep (its blocks of the same size; k8_out, v8_out [batch, T_out,
+ * G, d], k_scale_out, v_scale_out [batch, ceil(T_out / block), G]). With lens[b] <= keep all stay;
+ * else the `recent` last ones (0 <= recent <= keep) and, of those before them, the keep - recent of
+ * the largest weight [batch, G, T] (ties: the lower position; NaN counts as -infinity). Moved rows
+ * take the scale of their new block; a row whose scale does not change keeps its bits. Writes
+ *   kept [batch, G, keep] int32, the positions that stay, ascending, then -1;
+ *   lens_out [batch] int32 = min(lens[b], keep);  weight_out [batch, G, T_out], the weights that stay.
+ * No output may overlap an input. */
+int sgqa_cache8_evict(const sgqa_dims* dims, int block, const int32_t* lens, int keep, int recent, int T_out,
+                      const float* weight, const uint8_t* k8, const float* k_scale, const uint8_t* v8,
+                      const float* v_scale, uint8_t* k8_out, float* k_scale_out, uint8_t* v8_out,
+                      float* v_scale_out, float* weight_out, int32_t* kept, int32_t* lens_out, void* ws,
+                      size_t ws_bytes, void* stream);
+
 /* Failure-detection test hook (host-side setting, not for production use). While cta >= 0, the
  * decode attention CTA with that grid index in later sgqa_decode / sgqa_decode_fp8 calls issues
  * no loads, so its tensor-core issuer's wait for the first tile is never satisfied: the wait
