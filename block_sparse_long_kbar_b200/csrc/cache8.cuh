@@ -46,6 +46,7 @@ struct C8AttendArgs {
   float* lse;         // [batch, G, n_new * R]: log2 of each row's softmax sum
   float* part;
   int batch, T, Hq, G, d, block, n_new;
+  int nch, chunk_rows;  // set by the launch: chunks of rows per (sequence, group), rows of each
   int* status;
 };
 size_t cache8_part_bytes(int batch, int G, int rows, int d);
