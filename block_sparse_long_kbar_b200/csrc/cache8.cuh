@@ -46,7 +46,8 @@ struct C8AttendArgs {
   float* lse;         // [batch, G, n_new * R]: log2 of each row's softmax sum
   float* part;
   int batch, T, Hq, G, d, block, n_new;
-  int nch, chunk_rows;  // set by the launch: chunks of rows per (sequence, group), rows of each
+  // set by the launch: chunks of rows per (sequence, group), rows of each, log2 of block
+  int nch, chunk_rows, block_log2;
   int* status;
 };
 size_t cache8_part_bytes(int batch, int G, int rows, int d);

@@ -18,9 +18,12 @@
 // contiguous piece per CTA (one CTA per SM), so that ragged lengths, one long sequence and many
 // short ones all balance; the lengths are read on the device. A unit's pieces leave partial sums,
 // which a second kernel joins in the order of the tiles.
-// Roles: warp 0 issues TMA loads, warp 1 the MMAs, warps 2-3 split the rows of q, warps 4-7 and
-// 8-11 take tiles in turn (a thread per token) from S^T to P, warps 12-15 (a thread per head dim)
-// add O^T up. Waits are bounded as everywhere (tc_common.cuh).
+// Roles: warp 0 issues TMA loads, warp 1 the MMAs of S^T, warp 2 those of O^T, warps 3, 16 and 17
+// split the rows of q, warps 4-7 and 8-11 take tiles in turn from S^T to P, warps 12-15 (a thread per
+// head dim) add O^T up. Waits are bounded as everywhere (tc_common.cuh).
+// S^T is read in the 16x256b shape: a lane holds NR / 4 rows of 4 tokens (q's rows are placed so that
+// both terms of a row and pairs of rows land in one lane), so that row factors take NR / 4 registers,
+// maxima and sums over tokens start inside the thread, and products run on packed pairs.
 // The received weights need each row's final sum: a further pass over K recomputes the scores.
 #include <cuda.h>
 
@@ -34,7 +37,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNegMax = -3.4028234663852886e38f;  // maximum of a row that no token has reached
 constexpr int kTok = 128;                           // tokens per tile
 constexpr int kGridMax = 148;                       // one CTA per SM
-constexpr int kThreads = 512;
+constexpr int kThreads = 576;
 constexpr int kMaxNR = 32;                          // rows per unit; more make several units
 constexpr int kNever = 0x7FFFFFFF;
 
@@ -48,27 +51,29 @@ struct Cfg {
   static constexpr int kP = W ? 0 : kTok * N;
   static constexpr int kTmem = (W ? 2 : 4) * N < 32 ? 32 : (W ? 2 : 4) * N;
   static constexpr int kRowsT = D == 128 ? NR : NR / 2;  // rows per accumulating thread
+  static constexpr int q = NR / 4;                       // rows per lane of the softmax warps
 };
 
 template <int NR>
 struct Shared {
   uint64_t full[8], empty[8];
+  float scale[8][32];       // per stage: K scales of the tile's blocks, then V scales
   uint64_t s_full[2], s_empty[2], p_full[2], o_full[2], o_empty[2], q_full[2], q_empty[2];
   uint32_t tmem;
   volatile int abort_flag;
   int start_b, start_off, total;
-  int wsum[16];
+  int wsum[kThreads / 32];
   int nan_any[2];
   int nan_at[2][128];       // per head dim: first token not visible to all rows whose V is NaN there
   int wev[2][4];
   int e_tile[2];
-  float fac[2][NR];         // per unit parity: 2^e log2 e / sqrt(d) of a row
+  alignas(16) float fac[2][NR];  // per unit parity: 2^e log2 e / sqrt(d) of a row
   float lse[2][NR];
   int lim[2][NR];           // a row's own position; -1: no row
   float wmax[2][4][NR];
   float mt[2][NR];          // per softmax group: a row's maximum over the tile
-  float2 ab[2][NR];         // factors of the sums so far and of this tile
-  float2 acc_ab[2][NR];
+  float fa[2][NR], fb[2][NR];  // factors of the sums so far and of this tile
+  float acc_a[2][NR], acc_b[2][NR];
 };
 
 // The tiles of one CTA in order. unit = ((sequence, group), chunk of rows).
@@ -143,11 +148,78 @@ __host__ __device__ constexpr uint32_t idesc_f8(int N, bool a_mn, bool b_mn) {
 __device__ __forceinline__ uint64_t smem_desc_mnmajor_sw64_twice(const void* tile) {
   return (uint64_t)((smem_u32(tile) & 0x3FFFFu) >> 4) | ((uint64_t)(512 >> 4) << 32) | (1ull << 46) | (4ull << 61);
 }
-__device__ __forceinline__ float warp_max(float x) {
-  float y;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
-  return y;
+// 8 q columns of the warp's 32 TMEM lanes, as matrix fragments: c[16 h + ...]: lane / 4 + 8 e + 16 h is
+// the token, 8 j + 2 (lane % 4) + x the column of c[4 q h + 4 j + 2 e + x].
+template <int Q>
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&c)[8 * Q]);
+template <>
+__device__ __forceinline__ void tmem_ld_frag<2>(uint32_t taddr, uint32_t (&c)[16]) {
+  asm volatile(
+      "{ .reg .b32 t; add.u32 t, %16, 0x100000;\n"
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%16];\n"
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [t];\n"
+      "tcgen05.wait::ld.sync.aligned; }"
+      : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3]), "=r"(c[4]), "=r"(c[5]), "=r"(c[6]), "=r"(c[7]), "=r"(c[8]), "=r"(c[9]), "=r"(c[10]), "=r"(c[11]), "=r"(c[12]), "=r"(c[13]), "=r"(c[14]), "=r"(c[15])
+      : "r"(taddr)
+      : "memory");
 }
+template <>
+__device__ __forceinline__ void tmem_ld_frag<4>(uint32_t taddr, uint32_t (&c)[32]) {
+  asm volatile(
+      "{ .reg .b32 t; add.u32 t, %32, 0x100000;\n"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [t];\n"
+      "tcgen05.wait::ld.sync.aligned; }"
+      : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3]), "=r"(c[4]), "=r"(c[5]), "=r"(c[6]), "=r"(c[7]), "=r"(c[8]), "=r"(c[9]), "=r"(c[10]), "=r"(c[11]), "=r"(c[12]), "=r"(c[13]), "=r"(c[14]), "=r"(c[15]), "=r"(c[16]), "=r"(c[17]), "=r"(c[18]), "=r"(c[19]), "=r"(c[20]), "=r"(c[21]), "=r"(c[22]), "=r"(c[23]), "=r"(c[24]), "=r"(c[25]), "=r"(c[26]), "=r"(c[27]), "=r"(c[28]), "=r"(c[29]), "=r"(c[30]), "=r"(c[31])
+      : "r"(taddr)
+      : "memory");
+}
+template <>
+__device__ __forceinline__ void tmem_ld_frag<8>(uint32_t taddr, uint32_t (&c)[64]) {
+  asm volatile(
+      "{ .reg .b32 t; add.u32 t, %64, 0x100000;\n"
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n"
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [t];\n"
+      "tcgen05.wait::ld.sync.aligned; }"
+      : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3]), "=r"(c[4]), "=r"(c[5]), "=r"(c[6]), "=r"(c[7]), "=r"(c[8]), "=r"(c[9]), "=r"(c[10]), "=r"(c[11]), "=r"(c[12]), "=r"(c[13]), "=r"(c[14]), "=r"(c[15]), "=r"(c[16]), "=r"(c[17]), "=r"(c[18]), "=r"(c[19]), "=r"(c[20]), "=r"(c[21]), "=r"(c[22]), "=r"(c[23]), "=r"(c[24]), "=r"(c[25]), "=r"(c[26]), "=r"(c[27]), "=r"(c[28]), "=r"(c[29]), "=r"(c[30]), "=r"(c[31]), "=r"(c[32]), "=r"(c[33]), "=r"(c[34]), "=r"(c[35]), "=r"(c[36]), "=r"(c[37]), "=r"(c[38]), "=r"(c[39]), "=r"(c[40]), "=r"(c[41]), "=r"(c[42]), "=r"(c[43]), "=r"(c[44]), "=r"(c[45]), "=r"(c[46]), "=r"(c[47]), "=r"(c[48]), "=r"(c[49]), "=r"(c[50]), "=r"(c[51]), "=r"(c[52]), "=r"(c[53]), "=r"(c[54]), "=r"(c[55]), "=r"(c[56]), "=r"(c[57]), "=r"(c[58]), "=r"(c[59]), "=r"(c[60]), "=r"(c[61]), "=r"(c[62]), "=r"(c[63])
+      : "r"(taddr)
+      : "memory");
+}
+
+// pairs of fp32
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// A 4-byte copy to shared memory, and an arrival once this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
 
 // A warp's wait. After a wait has run out none waits any longer, but the roles go on through their
@@ -160,21 +232,22 @@ __device__ __forceinline__ void warp_wait(uint64_t* bar, uint32_t parity, volati
   __syncwarp();
 }
 
-// Sums of x[r] over the warp's lanes, in a fixed order; lane r (mod NR) gets row r's.
-template <int NR>
-__device__ __forceinline__ float warp_sums(float (&x)[NR], int lane) {
+// x[j] over the eight lanes that share rows (lane / 4), joined by op in a fixed order; the lane gets
+// row (lane / 4) mod Q.
+template <int Q, class Op>
+__device__ __forceinline__ float across_tokens(float (&x)[Q], int lane, Op op) {
 #pragma unroll
-  for (int h = NR / 2; h >= 1; h >>= 1) {
-    const bool up = lane & h;
+  for (int h = Q / 2; h >= 1; h >>= 1) {
+    const bool up = lane & (4 * h);
 #pragma unroll
     for (int i = 0; i < h; ++i) {
       const float give = up ? x[i] : x[i + h], have = up ? x[i + h] : x[i];
-      x[i] = have + __shfl_xor_sync(0xFFFFFFFFu, give, h);
+      x[i] = op(have, __shfl_xor_sync(0xFFFFFFFFu, give, 4 * h));
     }
   }
   float y = x[0];
 #pragma unroll
-  for (int h = NR; h < 32; h <<= 1) y += __shfl_xor_sync(0xFFFFFFFFu, y, h);
+  for (int h = Q; h < 8; h <<= 1) y = op(y, __shfl_xor_sync(0xFFFFFFFFu, y, 4 * h));
   return y;
 }
 
@@ -204,8 +277,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (lane == 0) sh.wsum[warp] = sum;
   if (tid == 0) {
     for (int i = 0; i < 8; ++i) {
-      tc::mbar_init(&sh.full[i], 1);
-      tc::mbar_init(&sh.empty[i], 1);
+      tc::mbar_init(&sh.full[i], 1 + 32);
+      tc::mbar_init(&sh.empty[i], W ? 1 + 4 : 1);  // the weights' pass reads scales after the MMA
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&sh.s_full[i], 1);
@@ -213,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(&sh.p_full[i], 128);
       tc::mbar_init(&sh.o_full[i], 1);
       tc::mbar_init(&sh.o_empty[i], 4);
-      tc::mbar_init(&sh.q_full[i], 64);
+      tc::mbar_init(&sh.q_full[i], 96);
       tc::mbar_init(&sh.q_empty[i], 1 + 8);
       sh.nan_any[i] = 0;
     }
@@ -226,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   int total = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) total += sh.wsum[i];
+  for (int i = 0; i < kThreads / 32; ++i) total += sh.wsum[i];
   // (every CTA below n has a tile: the CTAs between a unit's first and last have all written)
   const int n = min((int)gridDim.x, total), cta = (int)blockIdx.x;
   if (cta >= n) return;
@@ -245,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     int all = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < kThreads / 32; ++i) {
       if (i < warp) x += sh.wsum[i];
       all += sh.wsum[i];
     }
@@ -271,94 +344,108 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Part<D, NR> part(a.part, units);
 
   if (warp == 0) {
-    // ---- TMA: K and V tiles ----
-    if (lane == 0) {
-      int k = 0;
-      for (; w.left > 0; walk_next(w, a), ++k) {
-        const int st = k % C::kStages;
-        if (k >= C::kStages && !tc::mbar_wait(&sh.empty[st], (uint32_t)((k / C::kStages - 1) & 1), abort, a.status)) {
-          if (!*abort) report(a.status, SGQA_ERR_TIMEOUT);
-          *abort = 1;
-          break;
-        }
+    // ---- TMA: K and V tiles; a lane per block: their scales ----
+    const long nblk = ((long)a.T + a.block - 1) >> a.block_log2;
+    const int per = kTok >> a.block_log2, part_v = lane >> 4, j = lane & 15;
+    const float* scales = part_v ? a.c.vs : a.c.ks;
+    const bool mine = j < per && !(W && part_v);
+    int k = 0;
+    for (; w.left > 0; walk_next(w, a), ++k) {
+      const int st = k % C::kStages;
+      if (k >= C::kStages) warp_wait(&sh.empty[st], (uint32_t)((k / C::kStages - 1) & 1), abort, a.status);
+      if (*abort) break;
+      const int g = w.gu / a.nch;
+      if (lane == 0) {
         uint8_t* dst = sKV + st * C::kStage;
-        const int g = w.gu / a.nch, z = w.b * a.T + w.tile * kTok;
+        const int z = w.b * a.T + w.tile * kTok;
         tc::mbar_arrive_expect_tx(&sh.full[st], C::kStage);
         tc::tma_load_3d(dst, &map_k, &sh.full[st], 0, g, z);
         if (!W) tc::tma_load_3d(dst + C::kTile, &map_v, &sh.full[st], 0, g, z);
       }
-      // copies in flight land before the CTA leaves (all have, unless a wait ran out)
-      for (int j = max(0, k - C::kStages); j < k; ++j) {
-        volatile int none = 0;
-        tc::mbar_wait(&sh.full[j % C::kStages], (uint32_t)((j / C::kStages) & 1), &none);
-      }
+      const long blk = (long)w.tile * per + j;
+      if (mine && blk < nblk) cp_async4(&sh.scale[st][lane], scales + ((long)w.b * nblk + blk) * a.G + g);
+      cp_async_arrive(&sh.full[st]);
+    }
+    // copies in flight land before the CTA leaves (all have, unless a wait ran out)
+    cp_async_wait_all();
+    if (lane == 0) {
+      volatile int none = 0;
+      for (int i = max(0, k - C::kStages); i < k; ++i)
+        tc::mbar_wait(&sh.full[i % C::kStages], (uint32_t)((i / C::kStages) & 1), &none);
     }
   } else if (warp == 1) {
-    // ---- MMA ----
+    // ---- MMAs of S^T ----
     if (lane == 0) {
-      constexpr uint32_t id_s = idesc_f8(C::N, false, false), id_o = idesc_f8(C::N, true, true);
-      int k = 0, pv = 0, pieces = 0;
+      constexpr uint32_t id_s = idesc_f8(C::N, false, false);
+      const uint64_t dk = tc::smem_desc_kmajor(sKV, D), dq = tc::smem_desc_kmajor_noswz(sQ, 128, D * 8);
+      volatile int none = 0;
+      int k = 0, st = 0, ph = 0;
       bool ok = true;
-      auto issue_pv = [&]() -> bool {
-        const int pb = pv & 1, st = pv % C::kStages;
-        if (!tc::mbar_wait(&sh.p_full[pb], (uint32_t)((pv >> 1) & 1), abort, a.status)) return false;
-        if (pv >= 2 && !tc::mbar_wait(&sh.o_empty[pb], (uint32_t)(((pv >> 1) - 1) & 1), abort, a.status)) return false;
-        tc::fence_after_sync();
-        const uint8_t* v = sKV + st * C::kStage + C::kTile;
-        const uint8_t* p = sP + pb * C::kP;
-#pragma unroll
-        for (int kk = 0; kk < kTok / 32; ++kk) {
-          const uint64_t da = D == 128 ? tc::smem_desc_mnmajor_sw128(v + kk * 32 * D, 1024, 1024)
-                                       : smem_desc_mnmajor_sw64_twice(v + kk * 32 * D);
-          // P: [16 columns][128 tokens][16 bytes]: 8 tokens are 128 bytes, 16 columns 2048
-          mma_f8(tmem_o + (uint32_t)(pb * C::N), da, tc::smem_desc_kmajor_noswz(p + kk * 512, 128, 2048), id_o, kk > 0);
-        }
-        tc::mma_commit(&sh.empty[st]);
-        tc::mma_commit(&sh.o_full[pb]);
-        ++pv;
-        return true;
-      };
       for (; w.left > 0; walk_next(w, a), ++k) {
-        const int st = k % C::kStages, sb = k & 1;
-        if ((w.first && !tc::mbar_wait(&sh.q_full[w.piece & 1], (uint32_t)((w.piece >> 1) & 1), abort, a.status)) ||
-            !tc::mbar_wait(&sh.full[st], (uint32_t)((k / C::kStages) & 1), abort, a.status) ||
+        const int sb = k & 1, pb = w.piece & 1;
+        if ((w.first && !tc::mbar_wait(&sh.q_full[pb], (uint32_t)((w.piece >> 1) & 1), abort, a.status)) ||
+            !tc::mbar_wait(&sh.full[st], (uint32_t)ph, abort, a.status) ||
             (k >= 2 && !tc::mbar_wait(&sh.s_empty[sb], (uint32_t)(((k >> 1) - 1) & 1), abort, a.status))) {
           ok = false;
           break;
         }
         tc::fence_after_sync();
-        const uint8_t* kt = sKV + st * C::kStage;
-        const uint8_t* q = sQ + (w.piece & 1) * C::kQ;
+        const uint64_t da = dk + (uint32_t)(st * (C::kStage >> 4)), db = dq + (uint32_t)(pb * (C::kQ >> 4));
 #pragma unroll
         for (int kk = 0; kk < D / 32; ++kk)
-          mma_f8(tmem + (uint32_t)(sb * C::N), tc::smem_desc_kmajor(kt + kk * 32, D),
-                 tc::smem_desc_kmajor_noswz(q + kk * 256, 128, D * 8), id_s, kk > 0);
+          mma_f8(tmem + (uint32_t)(sb * C::N), da + kk * 2, db + kk * 16, id_s, kk > 0);
         tc::mma_commit(&sh.s_full[sb]);
         if (W) tc::mma_commit(&sh.empty[st]);
-        if (walk_last(w)) {
-          tc::mma_commit(&sh.q_empty[w.piece & 1]);
-          pieces = w.piece + 1;
-        }
-        if (!W && k > 0 && !(ok = issue_pv())) {
-          ++k;
-          break;
+        if (walk_last(w)) tc::mma_commit(&sh.q_empty[pb]);
+        if (++st == C::kStages) {
+          st = 0;
+          ph ^= 1;
         }
       }
-      if (!W && ok) ok = issue_pv();
       if (!ok) {
         if (!*abort) report(a.status, SGQA_ERR_TIMEOUT);
         *abort = 1;
       }
       // the MMAs in flight end before the CTA leaves
-      volatile int none = 0;
       if (k > 0) tc::mbar_wait(&sh.s_full[(k - 1) & 1], (uint32_t)(((k - 1) >> 1) & 1), &none);
-      const int freed = W ? k : pv;
-      for (int j = max(0, freed - C::kStages); j < freed; ++j)
-        tc::mbar_wait(&sh.empty[j % C::kStages], (uint32_t)((j / C::kStages) & 1), &none);
-      if (!W && pv > 0) tc::mbar_wait(&sh.o_full[(pv - 1) & 1], (uint32_t)(((pv - 1) >> 1) & 1), &none);
-      if (ok && pieces > 0) tc::mbar_wait(&sh.q_empty[(pieces - 1) & 1], (uint32_t)(((pieces - 1) >> 1) & 1), abort);
+      if (W && ok)
+        for (int j = max(0, k - C::kStages); j < k; ++j)
+          tc::mbar_wait(&sh.empty[j % C::kStages], (uint32_t)((j / C::kStages) & 1), abort);
+      if (ok) tc::mbar_wait(&sh.q_empty[w.piece & 1], (uint32_t)((w.piece >> 1) & 1), abort);
     }
-  } else if (warp < 4) {
+  } else if (warp == 2) {
+    // ---- MMAs of O^T ----
+    if (!W && lane == 0) {
+      constexpr uint32_t id_o = idesc_f8(C::N, true, true);
+      const uint64_t dv = D == 128 ? tc::smem_desc_mnmajor_sw128(sKV + C::kTile, 1024, 1024)
+                                   : smem_desc_mnmajor_sw64_twice(sKV + C::kTile);
+      // P: [16 columns][128 tokens][16 bytes]: 8 tokens are 128 bytes, 16 columns 2048
+      const uint64_t dp = tc::smem_desc_kmajor_noswz(sP, 128, 2048);
+      volatile int none = 0;
+      const int count = w.left;
+      int k = 0, st = 0;
+      for (; k < count; ++k) {
+        const int pb = k & 1;
+        if (!tc::mbar_wait(&sh.p_full[pb], (uint32_t)((k >> 1) & 1), abort, a.status) ||
+            (k >= 2 && !tc::mbar_wait(&sh.o_empty[pb], (uint32_t)(((k >> 1) - 1) & 1), abort, a.status))) {
+          if (!*abort) report(a.status, SGQA_ERR_TIMEOUT);
+          *abort = 1;
+          break;
+        }
+        tc::fence_after_sync();
+        const uint64_t da = dv + (uint32_t)(st * (C::kStage >> 4)), db = dp + (uint32_t)(pb * (C::kP >> 4));
+#pragma unroll
+        for (int kk = 0; kk < kTok / 32; ++kk)
+          mma_f8(tmem_o + (uint32_t)(pb * C::N), da + kk * (32 * D >> 4), db + kk * 32, id_o, kk > 0);
+        tc::mma_commit(&sh.empty[st]);
+        tc::mma_commit(&sh.o_full[pb]);
+        if (++st == C::kStages) st = 0;
+      }
+      if (k > 0) tc::mbar_wait(&sh.o_full[(k - 1) & 1], (uint32_t)(((k - 1) >> 1) & 1), &none);
+      for (int j = max(0, k - C::kStages); j < k; ++j)
+        tc::mbar_wait(&sh.empty[j % C::kStages], (uint32_t)((j / C::kStages) & 1), &none);
+    }
+  } else if (warp == 3 || warp >= 16) {
     // ---- a unit's rows of q as two E4M3 terms; a warp per row ----
     constexpr int kE = D / 32;
     for (; w.left > 0; walk_next(w, a)) {
@@ -367,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (w.piece >= 2) warp_wait(&sh.q_empty[pb], (uint32_t)(((w.piece >> 1) - 1) & 1), abort, a.status);
       uint8_t* dst = sQ + pb * C::kQ;
 #pragma unroll 4
-      for (int r = warp - 2; r < NR; r += 2) {
+      for (int r = warp == 3 ? 0 : warp - 15; r < NR; r += 3) {
         const int gr = r0 + r;
         const bool real = r < a.chunk_rows && gr < rows;
         uint32_t x[kE / 2];
@@ -406,8 +493,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           c2 |= t2 << (16 * e);
         }
         const int at = (lane * kE / 16) * 128 + lane * kE % 16;
-        uint8_t* p1 = dst + (r >> 3) * (D * 8) + (r & 7) * 16 + at;
-        uint8_t* p2 = dst + ((NR + r) >> 3) * (D * 8) + (r & 7) * 16 + at;
+        // columns 8 j + 2 i + x of S^T: row i q + (j / 2) 2 + x, term j % 2
+        const int jj = r % C::q, n1 = 16 * (jj >> 1) + 2 * (r / C::q) + (jj & 1), n2 = n1 + 8;
+        uint8_t* p1 = dst + (n1 >> 3) * (D * 8) + (n1 & 7) * 16 + at;
+        uint8_t* p2 = dst + (n2 >> 3) * (D * 8) + (n2 & 7) * 16 + at;
         if constexpr (kE == 4) {
           *reinterpret_cast<uint32_t*>(p1) = c1;
           *reinterpret_cast<uint32_t*>(p2) = c2;
@@ -418,175 +507,214 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           sh.fac[pb][r] = c8_pow2(ex) * (kLog2e / sqrtf((float)D));
           sh.lim[pb][r] = real ? w.L - a.n_new + gr / R : -1;
-          if (W) sh.lse[pb][r] = real ? a.lse[((long)w.b * a.G + g) * rows + gr] : 0.f;
+          if (W) sh.lse[pb][r] = real ? a.lse[((long)w.b * a.G + g) * rows + gr] : INFINITY;  // no row: 2^-inf
         }
       }
       tc::fence_proxy_async();
       tc::mbar_arrive(&sh.q_full[pb]);
     }
   } else if (warp < 12) {
-    // ---- a thread per token: scores, probabilities ----
-    const int wg = (warp >> 2) - 1, q4 = warp & 3, row = q4 * 32 + lane, t = tid & 127;
-    const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
-    const uint32_t ts = tmem + lane_base + (uint32_t)(wg * C::N);
-    const long nblk = (a.T + a.block - 1) / a.block;
-    float l[W ? 1 : NR];
+    // ---- scores, probabilities: lane = rows (lane % 4) q .. + q - 1 of tokens lane / 4 + 8 e ----
+    constexpr int q = C::q;
+    const int wg = (warp >> 2) - 1, q4 = warp & 3, t = tid & 127;
+    const int i = lane & 3, tok = q4 * 32 + (lane >> 2), row0 = i * q;
+    const uint32_t ts = tmem + ((uint32_t)(q4 * 32) << 16) + (uint32_t)(wg * C::N);
+    uint64_t fac[q / 2], l[q / 2];
 #pragma unroll
-    for (int r = 0; r < (W ? 1 : NR); ++r) l[r] = 0.f;
+    for (int j = 0; j < q / 2; ++j) fac[j] = l[j] = 0ull;
     float m_run = kNegMax;  // row t's, in the group's first threads
     int k = 0;
     for (; w.left > 0; walk_next(w, a), ++k) {
       const int pb = w.piece & 1;
-      if (w.first) warp_wait(&sh.q_full[pb], (uint32_t)((w.piece >> 1) & 1), abort, a.status);
+      if (w.first) {
+        warp_wait(&sh.q_full[pb], (uint32_t)((w.piece >> 1) & 1), abort, a.status);
+#pragma unroll
+        for (int j = 0; j < q / 2; ++j) fac[j] = pack2(sh.fac[pb][row0 + 2 * j], sh.fac[pb][row0 + 2 * j + 1]);
+      }
       if ((k & 1) == wg) {
-        const int u = w.tile * kTok + row, g = w.gu / a.nch;
-        const bool live = u < w.L;
+        const int u0 = w.tile * kTok + tok, g = w.gu / a.nch, st = k % C::kStages;
         const int vis = w.L - a.n_new;               // tokens up to here are visible to every row
         const bool edge = (w.tile + 1) * kTok - 1 > vis;
-        float sk = 0.f;
-        int ev = -126;
-        if (live) {
-          const long si = ((long)w.b * nblk + u / a.block) * a.G + g;
-          sk = c8_pow2(c8_scale_exponent(__ldg(a.c.ks + si)));
-          if (!W) ev = c8_scale_exponent(__ldg(a.c.vs + si));
+        const int uw = w.tile * kTok + q4 * 32 + (lane >> 2) + 8 * i;  // the token whose weight this lane writes
+        const long wi = ((long)w.b * a.G + g) * a.T + uw;
+        float sum = 0.f;
+        if constexpr (W) {
+          if (a.w_in && uw < vis) sum = a.w_in[wi];
+        }
+        warp_wait(&sh.s_full[wg], (uint32_t)((k >> 1) & 1), abort, a.status);
+        warp_wait(&sh.full[st], (uint32_t)((k / C::kStages) & 1), abort, a.status);
+        tc::fence_after_sync();
+        float sk[4], cv[4];
+        int we = -126;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool live = !edge || u0 + 8 * e < w.L;
+          const int sb = (tok + 8 * e) >> a.block_log2;
+          sk[e] = live ? c8_pow2(c8_scale_exponent(sh.scale[st][sb])) : 0.f;
+          const int ev = !W && live ? c8_scale_exponent(sh.scale[st][16 + sb]) : -126;
+          cv[e] = __int_as_float(ev);
+          we = max(we, ev);
         }
         if constexpr (W) {
-          const long wi = ((long)w.b * a.G + g) * a.T + u;
-          float sum = a.w_in && u < vis ? a.w_in[wi] : 0.f;
-          warp_wait(&sh.s_full[wg], (uint32_t)((k >> 1) & 1), abort, a.status);
-          tc::fence_after_sync();
-          float add = 0.f;
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&sh.empty[st]);
+        }
+        constexpr int qh = q < 8 ? q : 8;  // rows of one pass over S^T
+        uint64_t z[4][qh / 2];             // [token][pair of rows]
+        float add[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int h = 0; h < q / qh; ++h) {
+          uint32_t c[8 * qh];
+          tmem_ld_frag<qh>(ts + (uint32_t)(8 * qh * h), c);
+          if (h == q / qh - 1) {
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sh.s_empty[wg]);
+          }
+          const uint64_t sixteenth = pack2(0.0625f, 0.0625f);
+          const int rh = row0 + qh * h;
 #pragma unroll
-          for (int r0 = 0; r0 < NR; r0 += 16) {
-            constexpr int kH = NR < 16 ? NR : 16;
-            uint32_t c1[16], c2[16];
-            tc::tmem_ld16_nowait(ts + r0, c1);
-            if constexpr (NR >= 16) tc::tmem_ld16_nowait(ts + NR + r0, c2);
-            tc::tmem_wait_ld2(c1, c2);
-            if constexpr (NR < 16) {
+          for (int j = 0; j < qh / 2; ++j) {
+            // (the weights' pass takes the factors from shared memory: it may have several passes)
+            const uint64_t f = W ? pack2(sh.fac[pb][rh + 2 * j], sh.fac[pb][rh + 2 * j + 1]) : fac[j];
 #pragma unroll
-              for (int r = 0; r < kH; ++r) c2[r] = c1[NR + r];
-            }
-#pragma unroll
-            for (int r = 0; r < kH; ++r) {
-              const float z = fmaf(__uint_as_float(c2[r]), 0.0625f, __uint_as_float(c1[r])) * sh.fac[pb][r0 + r] * sk;
-              const float p = ex2_approx(z - sh.lse[pb][r0 + r]);
-              const int lim = sh.lim[pb][r0 + r];
-              add += lim >= u ? p : 0.f;
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t* x = c + 4 * qh * (e >> 1) + 8 * j + 2 * (e & 1);
+              const uint64_t q1 = pack2(__uint_as_float(x[0]), __uint_as_float(x[1]));
+              const uint64_t q2 = pack2(__uint_as_float(x[4]), __uint_as_float(x[5]));
+              z[e][j] = mul2(mul2(fma2(q2, sixteenth, q1), f), pack2(sk[e], sk[e]));
             }
           }
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&sh.s_empty[wg]);
-          if (live) a.w_out[wi] = sum + add;
-        } else {
-          warp_wait(&sh.s_full[wg], (uint32_t)((k >> 1) & 1), abort, a.status);
-          tc::fence_after_sync();
-          float z[NR];
-#pragma unroll
-          for (int r0 = 0; r0 < NR; r0 += 16) {
-            constexpr int kH = NR < 16 ? NR : 16;
-            uint32_t c1[16], c2[16];
-            tc::tmem_ld16_nowait(ts + r0, c1);
-            if constexpr (NR >= 16) tc::tmem_ld16_nowait(ts + NR + r0, c2);
-            tc::tmem_wait_ld2(c1, c2);
-            if constexpr (NR < 16) {
-#pragma unroll
-              for (int r = 0; r < kH; ++r) c2[r] = c1[NR + r];
-            }
-#pragma unroll
-            for (int r = 0; r < kH; ++r)
-              z[r0 + r] = fmaf(__uint_as_float(c2[r]), 0.0625f, __uint_as_float(c1[r])) * sh.fac[pb][r0 + r] * sk;
-          }
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&sh.s_empty[wg]);
           if (edge) {
 #pragma unroll
-            for (int r = 0; r < NR; ++r)
-              if (u > sh.lim[pb][r]) z[r] = -INFINITY;
-          }
-          // maxima of the tile; NaN counts for none (it reaches the sums by itself)
-          float mine = kNegMax;
+            for (int j = 0; j < qh / 2; ++j) {
+              const int lim0 = sh.lim[pb][rh + 2 * j], lim1 = sh.lim[pb][rh + 2 * j + 1];
 #pragma unroll
-          for (int r = 0; r < NR; ++r) {
-            const float x = warp_max(fmaxf(z[r], kNegMax));
-            if (lane == r) mine = x;
+              for (int e = 0; e < 4; ++e) {
+                const float2 x = unpack2(z[e][j]);
+                z[e][j] = pack2(u0 + 8 * e > lim0 ? -INFINITY : x.x, u0 + 8 * e > lim1 ? -INFINITY : x.y);
+              }
+            }
           }
-          const int we = __reduce_max_sync(0xFFFFFFFFu, ev);
-          if (lane < NR) sh.wmax[wg][q4][lane] = mine;
+          if constexpr (W) {
+#pragma unroll
+            for (int j = 0; j < qh / 2; ++j) {
+              const uint64_t lse = pack2(-sh.lse[pb][rh + 2 * j], -sh.lse[pb][rh + 2 * j + 1]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 x = unpack2(add2(z[e][j], lse)), y = unpack2(z[e][j]);
+                // (a masked token gets nothing from a row of NaN either)
+                add[e] += y.x == -INFINITY ? 0.f : ex2_approx(x.x);
+                add[e] += y.y == -INFINITY ? 0.f : ex2_approx(x.y);
+              }
+            }
+          }
+        }
+        if constexpr (W) {
+          // over the four lanes of a token; lane i gets token i
+          const bool up2 = i & 2, up1 = i & 1;
+          const float g0 = up2 ? add[0] : add[2], g1 = up2 ? add[1] : add[3];
+          const float h0 = (up2 ? add[2] : add[0]) + __shfl_xor_sync(0xFFFFFFFFu, g0, 2);
+          const float h1 = (up2 ? add[3] : add[1]) + __shfl_xor_sync(0xFFFFFFFFu, g1, 2);
+          const float tot = (up1 ? h1 : h0) + __shfl_xor_sync(0xFFFFFFFFu, up1 ? h0 : h1, 1);
+          if (uw < w.L) a.w_out[wi] = sum + tot;
+        } else {
+          // maxima of the tile; NaN counts for none (it reaches the sums by itself)
+          float mx[q];
+#pragma unroll
+          for (int j = 0; j < q / 2; ++j) {
+            float2 x = make_float2(kNegMax, kNegMax);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 y = unpack2(z[e][j]);
+              x.x = fmaxf(x.x, y.x);
+              x.y = fmaxf(x.y, y.y);
+            }
+            mx[2 * j] = x.x;
+            mx[2 * j + 1] = x.y;
+          }
+          const float mine = across_tokens<q>(mx, lane, [](float x, float y) { return fmaxf(x, y); });
+          we = __reduce_max_sync(0xFFFFFFFFu, we);
+          if ((lane >> 2) < q) sh.wmax[wg][q4][row0 + (lane >> 2)] = mine;
           if (lane == 0) sh.wev[wg][q4] = we;
-          group_sync(1 + wg);
           // the P buffer and the tile's numbers two tiles back have been read
           if (k >= 2) warp_wait(&sh.o_empty[wg], (uint32_t)(((k >> 1) - 1) & 1), abort, a.status);
+          group_sync(1 + wg);
           if (t < NR) {
             const float mt = fmaxf(fmaxf(sh.wmax[wg][0][t], sh.wmax[wg][1][t]), fmaxf(sh.wmax[wg][2][t], sh.wmax[wg][3][t]));
             const float mn = fmaxf(m_run, mt);
             sh.mt[wg][t] = mt;
-            sh.ab[wg][t] = make_float2(ex2_approx(m_run - mn), ex2_approx(mt - mn));
+            sh.fa[wg][t] = ex2_approx(m_run - mn);
+            sh.fb[wg][t] = ex2_approx(mt - mn);
             m_run = mn;
           }
           const int et = max(max(sh.wev[wg][0], sh.wev[wg][1]), max(sh.wev[wg][2], sh.wev[wg][3]));
           if (t == 0) sh.e_tile[wg] = et;
-          group_sync(1 + wg);
-          const float cv = 448.f * c8_pow2(max(-126, ev - et));
-          uint8_t* pd = sP + wg * C::kP + row * 16;
-#pragma unroll
-          for (int r0 = 0; r0 < NR; r0 += 16) {
-            constexpr int kH = NR < 16 ? NR : 16;
-            uint32_t p1[kH / 4], p2[kH / 4];
-#pragma unroll
-            for (int r = 0; r < kH; r += 2) {
-              float y[2];
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const float p = ex2_approx(z[r0 + r + e] - sh.mt[wg][r0 + r + e]);
-                const float2 ab = sh.ab[wg][r0 + r + e];
-                l[r0 + r + e] = fmaf(l[r0 + r + e], ab.x, p * ab.y);
-                y[e] = p * cv;
-              }
-              const uint32_t t1 = c8_encode2(y[0], y[1]);
-              const float2 f = c8_decode2(t1);
-              const uint32_t t2 = c8_encode2((y[0] - f.x) * 28.f, (y[1] - f.y) * 28.f);
-              if (r & 2) {
-                p1[r / 4] |= t1 << 16;
-                p2[r / 4] |= t2 << 16;
-              } else {
-                p1[r / 4] = t1;
-                p2[r / 4] = t2;
-              }
-            }
-            if constexpr (NR < 16) {
-              *reinterpret_cast<uint4*>(pd) = make_uint4(p1[0], p1[1], p2[0], p2[1]);
-            } else {
-              *reinterpret_cast<uint4*>(pd + (r0 / 16) * 2048) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
-              *reinterpret_cast<uint4*>(pd + ((NR + r0) / 16) * 2048) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
-            }
-          }
           if (edge) {
             // A zero probability must not meet a NaN code: rows behind the last token become zeros,
             // and a NaN of a token that some row does not see is noted and taken out; the rows that
             // see it get it back at the end.
-            warp_wait(&sh.full[k % C::kStages], (uint32_t)((k / C::kStages) & 1), abort, a.status);
-            uint8_t* v = sKV + (k % C::kStages) * C::kStage + C::kTile + row * D;
-            if (!live) {
+            const int u = w.tile * kTok + t;
+            uint8_t* v = sKV + st * C::kStage + C::kTile + t * D;
+            if (u >= w.L) {
 #pragma unroll
               for (int c = 0; c < D / 16; ++c) *reinterpret_cast<uint4*>(v + c * 16) = make_uint4(0u, 0u, 0u, 0u);
             } else if (u > vis) {
-              for (int c = 0; c < D / 16; ++c) {
-                for (int x = 0; x < 16; ++x) {
-                  uint8_t* code = v + v_chunk<D>(row, c) * 16 + x;
-                  if ((*code & 0x7F) == 0x7F) {
-                    *code = 0;
-                    atomicMin(&sh.nan_at[pb][c * 16 + x], u);
-                    sh.nan_any[pb] = 1;
-                  }
-                }
+              for (int c = 0; c < D / 4; ++c) {
+                uint32_t* p = reinterpret_cast<uint32_t*>(v + v_chunk<D>(t, c >> 2) * 16 + (c & 3) * 4);
+                const uint32_t nan = __vcmpeq4(*p & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                if (!nan) continue;
+                *p &= ~nan;
+                sh.nan_any[pb] = 1;
+                for (int x = 0; x < 4; ++x)
+                  if (nan >> (8 * x) & 1u) atomicMin(&sh.nan_at[pb][c * 4 + x], u);
               }
+            }
+          }
+          group_sync(1 + wg);
+          uint64_t mt[q / 2], ps[q / 2];
+#pragma unroll
+          for (int j = 0; j < q / 2; ++j) {
+            mt[j] = pack2(-sh.mt[wg][row0 + 2 * j], -sh.mt[wg][row0 + 2 * j + 1]);
+            ps[j] = 0ull;
+          }
+          uint8_t* pd = sP + wg * C::kP + (i * 2 * q / 16) * 2048 + (i * 2 * q % 16) + tok * 16;
+          const uint64_t c28 = pack2(28.f, 28.f);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float cs = 448.f * c8_pow2(max(-126, __float_as_int(cv[e]) - et));
+            const uint64_t c2 = pack2(cs, cs);
+            uint32_t p1[q / 2], p2[q / 2];  // two codes each
+#pragma unroll
+            for (int j = 0; j < q / 2; ++j) {
+              const float2 x = unpack2(add2(z[e][j], mt[j]));
+              const uint64_t p = pack2(ex2_approx(x.x), ex2_approx(x.y));
+              ps[j] = add2(ps[j], p);
+              const uint64_t y2 = mul2(p, c2);
+              const float2 y = unpack2(y2);
+              p1[j] = c8_encode2(y.x, y.y);
+              const float2 f = c8_decode2(p1[j]);
+              const float2 r = unpack2(mul2(add2(y2, pack2(-f.x, -f.y)), c28));
+              p2[j] = c8_encode2(r.x, r.y);
+            }
+            uint8_t* d = pd + e * 128;
+            if constexpr (q == 8) {
+              *reinterpret_cast<uint4*>(d) = make_uint4(p1[0] | p1[1] << 16, p1[2] | p1[3] << 16, p2[0] | p2[1] << 16,
+                                                        p2[2] | p2[3] << 16);
+            } else if constexpr (q == 4) {
+              *reinterpret_cast<uint2*>(d) = make_uint2(p1[0] | p1[1] << 16, p2[0] | p2[1] << 16);
+            } else {
+              *reinterpret_cast<uint32_t*>(d) = p1[0] | p2[0] << 16;
             }
           }
           tc::fence_proxy_async();
           tc::mbar_arrive(&sh.p_full[wg]);
+#pragma unroll
+          for (int j = 0; j < q / 2; ++j) {
+            const uint64_t fa = pack2(sh.fa[wg][row0 + 2 * j], sh.fa[wg][row0 + 2 * j + 1]);
+            const uint64_t fb = pack2(sh.fb[wg][row0 + 2 * j], sh.fb[wg][row0 + 2 * j + 1]);
+            l[j] = fma2(l[j], fa, mul2(ps[j], fb));
+          }
         }
       }
       if (walk_last(w)) {
@@ -595,12 +723,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (!W) {
           // this piece's sums
           const long slot = (long)w.b * units_b + w.gu + blockIdx.x;
-          const float s = warp_sums<NR>(l, lane);
-          if (lane < NR) part.l(slot)[(wg * 4 + q4) * NR + lane] = s;
+          float x[q];
+#pragma unroll
+          for (int j = 0; j < q / 2; ++j) {
+            const float2 y = unpack2(l[j]);
+            x[2 * j] = y.x;
+            x[2 * j + 1] = y.y;
+            l[j] = 0ull;
+          }
+          const float s = across_tokens<q>(x, lane, [](float x, float y) { return x + y; });
+          if ((lane >> 2) < q) part.l(slot)[(wg * 4 + q4) * NR + row0 + (lane >> 2)] = s;
           if (t < NR) part.lm(slot)[wg * NR + t] = m_run;
           m_run = kNegMax;
-#pragma unroll
-          for (int r = 0; r < NR; ++r) l[r] = 0.f;
         }
       }
     }
@@ -608,10 +742,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- a thread per head dim: outputs ----
     const int q4 = warp & 3, t = tid & 127;
     const int dim = D == 128 ? t : t & 63, rb = D == 128 ? 0 : (t >> 6) * C::kRowsT;
-    const uint32_t to = tmem_o + ((uint32_t)(q4 * 32) << 16) + (uint32_t)rb;
-    float o[C::kRowsT];
+    // columns of O^T: rows i q .. of the first terms, then of the second, for i = 0 .. 3
+    const uint32_t to = tmem_o + ((uint32_t)(q4 * 32) << 16) + (uint32_t)(C::kRowsT < 8 ? 0 : 2 * rb);
+    uint64_t o[C::kRowsT / 2];
 #pragma unroll
-    for (int r = 0; r < C::kRowsT; ++r) o[r] = 0.f;
+    for (int r = 0; r < C::kRowsT / 2; ++r) o[r] = 0ull;
     float m_run = kNegMax;
     int e_run = -126;
     int first_tile = 0;
@@ -623,42 +758,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int et = sh.e_tile[sb], en = max(e_run, et);
       if (t < NR) {
         const float mt = sh.mt[sb][t], mn = fmaxf(m_run, mt);
-        sh.acc_ab[sb][t] = make_float2(ex2_approx(m_run - mn) * c8_pow2(max(-126, e_run - en)),
-                                       ex2_approx(mt - mn) * c8_pow2(max(-126, et - en)) * (1.f / 448.f));
+        sh.acc_a[sb][t] = ex2_approx(m_run - mn) * c8_pow2(max(-126, e_run - en));
+        sh.acc_b[sb][t] = ex2_approx(mt - mn) * c8_pow2(max(-126, et - en)) * (1.f / 448.f);
         m_run = mn;
       }
       e_run = en;
       group_sync(3);
       warp_wait(&sh.o_full[sb], (uint32_t)((k >> 1) & 1), abort, a.status);
       tc::fence_after_sync();
+      const uint64_t c28 = pack2(1.f / 28.f, 1.f / 28.f);
 #pragma unroll
       for (int r0 = 0; r0 < C::kRowsT; r0 += 16) {
-        constexpr int kH = C::kRowsT < 16 ? C::kRowsT : 16;
-        uint32_t c1[16], c2[16];
-        if constexpr (NR >= 16) {
-          // 16 columns of each term (with 8 rows a thread the upper half is not used)
-          tc::tmem_ld16_nowait(to + (uint32_t)(sb * C::N + r0), c1);
-          tc::tmem_ld16_nowait(to + (uint32_t)(sb * C::N + NR + r0) - (kH < 16 && D == 64 ? (uint32_t)rb : 0u), c2);
-        } else {
-          tc::tmem_ld16_nowait(to - (uint32_t)rb + (uint32_t)(sb * C::N), c1);
-        }
-        tc::tmem_wait_ld2(c1, c2);
+        constexpr int kH = C::kRowsT < 16 ? C::kRowsT : 16, q = C::q;
+        uint32_t c[2][16];
+        tc::tmem_ld16_nowait(to + (uint32_t)(sb * C::N + 2 * r0), c[0]);
+        if constexpr (kH == 16) tc::tmem_ld16_nowait(to + (uint32_t)(sb * C::N + 2 * r0 + 16), c[1]);
+        tc::tmem_wait_ld2(c[0], c[1]);
 #pragma unroll
-        for (int r = 0; r < kH; ++r) {
-          float x1, x2;
-          if constexpr (NR >= 16) {
-            x1 = __uint_as_float(c1[r]);
-            if constexpr (kH < 16) x2 = __uint_as_float(rb ? c2[kH + r] : c2[r]);
-            else x2 = __uint_as_float(c2[r]);
-          } else if constexpr (D == 128) {
-            x1 = __uint_as_float(c1[r]);
-            x2 = __uint_as_float(c1[NR + r]);
-          } else {
-            x1 = __uint_as_float(rb ? c1[C::kRowsT + r] : c1[r]);
-            x2 = __uint_as_float(rb ? c1[NR + C::kRowsT + r] : c1[NR + r]);
+        for (int r = 0; r < kH; r += 2) {
+          const int h = r >> 3, x = (r & 7) / q * 2 * q + (r & 7) % q;
+          float x1 = __uint_as_float(c[h][x]), y1 = __uint_as_float(c[h][x + 1]);
+          float x2 = __uint_as_float(c[h][x + q]), y2 = __uint_as_float(c[h][x + q + 1]);
+          if constexpr (C::kRowsT < 8) {  // the upper rows' threads: 8 columns on
+            if (rb) {
+              x1 = __uint_as_float(c[0][x + 8]), y1 = __uint_as_float(c[0][x + 9]);
+              x2 = __uint_as_float(c[0][x + q + 8]), y2 = __uint_as_float(c[0][x + q + 9]);
+            }
           }
-          const float2 ab = sh.acc_ab[sb][rb + r0 + r];
-          o[r0 + r] = fmaf(o[r0 + r], ab.x, fmaf(x2, 1.f / 28.f, x1) * ab.y);
+          const int rr = rb + r0 + r;
+          const uint64_t fa = pack2(sh.acc_a[sb][rr], sh.acc_a[sb][rr + 1]);
+          const uint64_t fb = pack2(sh.acc_b[sb][rr], sh.acc_b[sb][rr + 1]);
+          o[(r0 + r) / 2] = fma2(o[(r0 + r) / 2], fa, mul2(fma2(pack2(x2, y2), c28, pack2(x1, y1)), fb));
         }
       }
       tc::fence_before_sync();
@@ -668,8 +798,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (sh.nan_any[pb]) {
           const int np = sh.nan_at[pb][dim], r0 = (w.gu % a.nch) * a.chunk_rows + rb;
 #pragma unroll
-          for (int r = 0; r < C::kRowsT; ++r)
-            if (np <= w.L - a.n_new + (r0 + r) / R) o[r] = __int_as_float(0x7FC00000);
+          for (int r = 0; r < C::kRowsT; r += 2) {
+            const float nan = __int_as_float(0x7FC00000);
+            const float2 y = unpack2(o[r / 2]);
+            o[r / 2] = pack2(np <= w.L - a.n_new + (r0 + r) / R ? nan : y.x,
+                             np <= w.L - a.n_new + (r0 + r + 1) / R ? nan : y.y);
+          }
         }
         group_sync(3);
         sh.nan_at[pb][t] = kNever;
@@ -680,9 +814,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (last) {
         float* po = part.o(slot) + rb * D + dim;
 #pragma unroll
-        for (int r = 0; r < C::kRowsT; ++r) {
-          po[r * D] = o[r];
-          o[r] = 0.f;
+        for (int r = 0; r < C::kRowsT; r += 2) {
+          const float2 y = unpack2(o[r / 2]);
+          po[r * D] = y.x;
+          po[(r + 1) * D] = y.y;
+          o[r / 2] = 0ull;
         }
         if (t < NR) part.m(slot)[t] = m_run;
         if (t == 0) {
@@ -703,39 +839,82 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the pieces of a unit in the order of their tiles: a CTA per (sequence, group, row), a thread
-// per head dim.
+// Joins the pieces of a unit in the order of their tiles: a CTA per (sequence, group, row). The
+// factors of 256 pieces at a time are made by a thread each, then warps take the pieces in turn.
+constexpr int kJoinThr = 256;
 template <int D, int NR>
-__global__ void __launch_bounds__(D) cache8_join_kernel(C8AttendArgs a) {
+__global__ void __launch_bounds__(kJoinThr) cache8_join_kernel(C8AttendArgs a) {
+  constexpr int kV = D / 32;
+  __shared__ float s_f[kJoinThr], s_o[kJoinThr / 32][D], s_m[kJoinThr / 32], s_l[kJoinThr / 32];
+  __shared__ int s_e[kJoinThr / 32];
   if (tc::grid_timed_out(a.status)) return;
   const int R = a.Hq / a.G, rows = a.n_new * R;
   const int gr = blockIdx.x % rows, bg = blockIdx.x / rows, b = bg / a.G, g = bg % a.G;
-  const int r = gr % a.chunk_rows, t = threadIdx.x;
+  const int r = gr % a.chunk_rows, t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const long unit = (long)bg * a.nch + gr / a.chunk_rows;
   const int L = len_of(a, b);
   const Part<D, NR> part(a.part, (long)a.batch * a.G * a.nch);
-  float den = 0.f, num = 0.f, m = kNegMax;
+  const long at = (((long)b * a.n_new + gr / R) * a.Hq + (long)g * R + gr % R) * D;
+  const bool some = L > a.n_new - 1 - gr / R;
+  const int c0 = some ? part.first[unit] : 0, n = some ? part.last[unit] - c0 + 1 : 0;
+  float m = kNegMax, den = 0.f, o[kV];
   int e = -126;
-  if (L > a.n_new - 1 - gr / R) {
-    const int c0 = part.first[unit], c1 = part.last[unit];
-    for (int c = c0; c <= c1; ++c) {
-      m = fmaxf(m, part.m(unit + c)[r]);
-      e = max(e, *part.e(unit + c));
-    }
-    for (int c = c0; c <= c1; ++c) {
-      const long slot = unit + c;
-      const float f = ex2_approx(part.m(slot)[r] - m) * c8_pow2(max(-126, *part.e(slot) - e));
-      num = fmaf(part.o(slot)[r * D + t], f, num);
+#pragma unroll
+  for (int x = 0; x < kV; ++x) o[x] = 0.f;
+  for (int c = t; c < n; c += kJoinThr) {
+    m = fmaxf(m, part.m(unit + c0 + c)[r]);
+    e = max(e, *part.e(unit + c0 + c));
+  }
+#pragma unroll
+  for (int h = 16; h; h >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, h));
+  e = __reduce_max_sync(0xFFFFFFFFu, e);
+  if (lane == 0) {
+    s_m[warp] = m;
+    s_e[warp] = e;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int x = 0; x < kJoinThr / 32; ++x) {
+    m = fmaxf(m, s_m[x]);
+    e = max(e, s_e[x]);
+  }
+  for (int p0 = 0; p0 < n; p0 += kJoinThr) {
+    const int c = p0 + t;
+    if (c < n) {
+      const long slot = unit + c0 + c;
+      s_f[t] = ex2_approx(part.m(slot)[r] - m) * c8_pow2(max(-126, *part.e(slot) - e));
 #pragma unroll
       for (int wg = 0; wg < 2; ++wg) {
         const float* l = part.l(slot) + wg * 4 * NR + r;
         den = fmaf((l[0] + l[NR]) + (l[2 * NR] + l[3 * NR]), ex2_approx(part.lm(slot)[wg * NR + r] - m), den);
       }
     }
+    __syncthreads();
+#pragma unroll 4
+    for (int x = warp; x < min(kJoinThr, n - p0); x += kJoinThr / 32) {
+      const float* src = part.o(unit + c0 + p0 + x) + r * D + lane * kV;
+      const float f = s_f[x];
+#pragma unroll
+      for (int v = 0; v < kV; ++v) o[v] = fmaf(src[v], f, o[v]);
+    }
+    __syncthreads();
   }
-  const long at = (((long)b * a.n_new + gr / R) * a.Hq + (long)g * R + gr % R) * D + t;
-  const float y = den == 0.f ? 0.f : num / den * c8_pow2(e);
-  a.out[at] = f32_to_bf16_rne(y * sigmoid_fast(bf16_to_f32(__ldg(a.gate + at))));
+#pragma unroll
+  for (int h = 16; h; h >>= 1) den += __shfl_xor_sync(0xFFFFFFFFu, den, h);
+  if (lane == 0) s_l[warp] = den;
+#pragma unroll
+  for (int v = 0; v < kV; ++v) s_o[warp][lane * kV + v] = o[v];
+  __syncthreads();
+  den = 0.f;
+#pragma unroll
+  for (int x = 0; x < kJoinThr / 32; ++x) den += s_l[x];
+  if (t < D) {
+    float num = 0.f;
+#pragma unroll
+    for (int x = 0; x < kJoinThr / 32; ++x) num += s_o[x][t];
+    const float y = den == 0.f ? 0.f : num / den * c8_pow2(e);
+    a.out[at + t] = f32_to_bf16_rne(y * sigmoid_fast(bf16_to_f32(__ldg(a.gate + at + t))));
+  }
   if (t == 0 && a.w_out) a.lse[(long)bg * rows + gr] = den == 0.f ? 0.f : m + log2f(den);
 }
 
@@ -775,6 +954,7 @@ cudaError_t launch_main(const CUtensorMap& mk, const CUtensorMap& mv, C8AttendAr
   if (e != cudaSuccess) return e;
   a.nch = nch;
   a.chunk_rows = chunk_rows;
+  a.block_log2 = a.block == 8 ? 3 : a.block == 16 ? 4 : a.block == 32 ? 5 : a.block == 64 ? 6 : 7;
   const long tiles = (long)a.batch * a.G * nch * ((a.T + kTok - 1) / kTok);
   const unsigned grid = (unsigned)(tiles < kGridMax ? tiles : kGridMax);
   cache8_attend_kernel<D, NR, W><<<grid, kThreads, kSmem, s>>>(mk, mv, a);
@@ -799,7 +979,7 @@ cudaError_t launch_rows(const CUtensorMap& mk, const CUtensorMap& mv, C8AttendAr
   const int rows = a.n_new * (a.Hq / a.G);
   const long ctas = (long)a.batch * a.G * rows;
   if (ctas > 0x7FFFFFFFL) return cudaErrorInvalidConfiguration;
-  cache8_join_kernel<D, NR><<<(unsigned)ctas, D, 0, s>>>(a);
+  cache8_join_kernel<D, NR><<<(unsigned)ctas, kJoinThr, 0, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess || !a.w_out) return e;
   return rw.nch == 1 ? launch_main<D, NR, true>(mk, mv, a, 1, rows, s) : launch_main<D, 64, true>(mk, mv, a, 1, rows, s);
 }
