@@ -18,8 +18,8 @@
 // contiguous piece per CTA (one CTA per SM), so that ragged lengths, one long sequence and many
 // short ones all balance; the lengths are read on the device. A unit's pieces leave partial sums,
 // which a second kernel joins in the order of the tiles.
-// Roles: warp 0 issues TMA loads, warp 1 the MMAs of S^T, warp 2 those of O^T, warps 3, 16 and 17
-// split the rows of q, warps 4-7 and 8-11 take tiles in turn from S^T to P, warps 12-15 (a thread per
+// Roles: warp 0 issues TMA loads, warp 1 the MMAs of S^T, warp 2 those of O^T, warp 3
+// splits the rows of q, warps 4-7 and 8-11 take tiles in turn from S^T to P, warps 12-15 (a thread per
 // head dim) add O^T up. Waits are bounded as everywhere (tc_common.cuh).
 // S^T is read in the 16x256b shape: a lane holds NR / 4 rows of 4 tokens (q's rows are placed so that
 // both terms of a row and pairs of rows land in one lane), so that row factors take NR / 4 registers,
@@ -37,7 +37,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNegMax = -3.4028234663852886e38f;  // maximum of a row that no token has reached
 constexpr int kTok = 128;                           // tokens per tile
 constexpr int kGridMax = 148;                       // one CTA per SM
-constexpr int kThreads = 576;
+constexpr int kThreads = 512;
 constexpr int kMaxNR = 32;                          // rows per unit; more make several units
 constexpr int kNever = 0x7FFFFFFF;
 
@@ -74,10 +74,12 @@ struct Shared {
   alignas(16) float acc_a[2][NR], acc_b[2][NR];  // factors of the sums so far and of this tile
 };
 
-// The tiles of one CTA in order. unit = ((sequence, group), chunk of rows).
+// The tiles of one CTA in order, a piece of a unit at a time: tiles [t0, t1) of unit ((sequence b,
+// group g), chunk ch of its rows). A loop over a piece's tiles has nothing else to keep track of: with
+// four roles on every scheduler, instruction fetch is what short loops are for.
 struct Walk {
-  int b, g, ch, tile, ntiles, L, left, piece;
-  bool first;  // the first tile of this CTA's piece of the unit
+  int b, g, ch, L, ntiles, t0, t1, left;  // left: tiles of this and later pieces
+  int piece, k;                           // pieces and tiles of this CTA before
 };
 __device__ __forceinline__ int tiles_of(int L) { return (L + kTok - 1) / kTok; }
 __device__ __forceinline__ int len_of(const C8AttendArgs& a, int b) {
@@ -91,28 +93,29 @@ __device__ __forceinline__ void walk_begin(Walk& w, const C8AttendArgs& a, int b
   const int gu = off / w.ntiles;
   w.g = gu / a.nch;
   w.ch = gu % a.nch;
-  w.tile = off % w.ntiles;
+  w.t0 = off % w.ntiles;
   w.left = left;
-  w.piece = 0;
-  w.first = true;
+  w.t1 = min(w.ntiles, w.t0 + left);
+  w.piece = w.k = 0;
 }
-__device__ __forceinline__ bool walk_last(const Walk& w) { return w.left == 1 || w.tile + 1 == w.ntiles; }
 __device__ __forceinline__ void walk_next(Walk& w, const C8AttendArgs& a) {
-  w.first = false;
-  if (--w.left == 0) return;
-  if (++w.tile < w.ntiles) return;
-  w.tile = 0;
-  w.first = true;
+  w.left -= w.t1 - w.t0;
+  w.k += w.t1 - w.t0;
   ++w.piece;
-  if (++w.ch < a.nch) return;
-  w.ch = 0;
-  if (++w.g < a.G) return;
-  w.g = 0;
-  do {
-    ++w.b;
-    w.L = len_of(a, w.b);
-  } while (w.L == 0);
-  w.ntiles = tiles_of(w.L);
+  if (w.left == 0) return;
+  if (++w.ch == a.nch) {
+    w.ch = 0;
+    if (++w.g == a.G) {
+      w.g = 0;
+      do {
+        ++w.b;
+        w.L = len_of(a, w.b);
+      } while (w.L == 0);
+      w.ntiles = tiles_of(w.L);
+    }
+  }
+  w.t0 = 0;
+  w.t1 = min(w.ntiles, w.left);
 }
 
 // Per launch: partial sums of every piece, and the CTAs that hold a unit's first and last tile.
@@ -260,6 +263,84 @@ __device__ __forceinline__ int v_chunk(int row, int c) {
   return D == 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3);
 }
 
+// Rows r_begin, r_begin + r_step, .. of a unit's q as two E4M3 terms, and what else a row needs; a warp
+// per row, eight rows' loads at a time.
+template <int D, int NR, bool W>
+__device__ __forceinline__ void split_q(const C8AttendArgs& a, const Walk& w, Shared<NR>& sh, uint8_t* sQ, int r_begin,
+                                        int r_step, int lane) {
+  using C = Cfg<D, NR, W>;
+  constexpr int kE = D / 32;
+  const int R = a.Hq / a.G, rows = a.n_new * R;
+  const int pb = w.piece & 1, r0 = w.ch * a.chunk_rows, real = min(a.chunk_rows, rows - r0);
+  uint8_t* dst = sQ + pb * C::kQ;
+  for (int r = r_begin + lane * r_step; r < NR; r += 32 * r_step) {
+    sh.lim[pb][r] = r < real ? w.L - a.n_new + (r0 + r) / R : -1;
+    // (no row: 2^-inf)
+    if (W) sh.lse[pb][r] = r < real ? a.lse[((long)w.b * a.G + w.g) * rows + r0 + r] : INFINITY;
+  }
+  for (int r8 = r_begin; r8 < NR; r8 += 8 * r_step) {
+    uint32_t x[8][kE / 2];
+#pragma unroll
+    for (int y = 0; y < 8; ++y) {
+      const int r = r8 + y * r_step;
+#pragma unroll
+      for (int e = 0; e < kE / 2; ++e) x[y][e] = 0u;
+      if (r < real) {
+        const int gr = r0 + r;
+        const long src = (((long)w.b * a.n_new + gr / R) * a.Hq + (long)w.g * R + gr % R) * D + lane * kE;
+        if constexpr (kE == 4) {
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(a.q + src));
+          x[y][0] = v.x;
+          x[y][1] = v.y;
+        } else {
+          x[y][0] = __ldg(reinterpret_cast<const uint32_t*>(a.q + src));
+        }
+      }
+    }
+#pragma unroll
+    for (int y = 0; y < 8; ++y) {
+      const int r = r8 + y * r_step;
+      if (r >= NR) break;
+      uint32_t amax = 0u;
+#pragma unroll
+      for (int e = 0; e < kE / 2; ++e) {
+        const uint32_t lo = x[y][e] & 0x7FFFu, hi = (x[y][e] >> 16) & 0x7FFFu;
+        amax = max(amax, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+      }
+      amax = __reduce_max_sync(0xFFFFFFFFu, amax);
+      const int ex = c8_exponent(amax << 16);
+      const float inv = c8_pow2(-ex);
+      uint32_t c1 = 0u, c2 = 0u;
+#pragma unroll
+      for (int e = 0; e < kE / 2; ++e) {
+        const float y0 = bf16_lo(x[y][e]) * inv, y1 = bf16_hi(x[y][e]) * inv;
+        uint32_t t1 = c8_encode2(y0, y1);
+        const float2 f = c8_decode2(t1);
+        const uint32_t t2 = c8_encode2((y0 - f.x) * 16.f, (y1 - f.y) * 16.f);
+        // an infinity becomes NaN, as which it would end in the scores
+        if ((x[y][e] & 0x7F80u) == 0x7F80u) t1 |= 0x7Fu;
+        if ((x[y][e] & 0x7F800000u) == 0x7F800000u) t1 |= 0x7F00u;
+        c1 |= t1 << (16 * e);
+        c2 |= t2 << (16 * e);
+      }
+      // columns 8 j + 2 i + x of S^T: row i q + (j / 2) 2 + x, term j % 2
+      const int at = (lane * kE / 16) * 128 + lane * kE % 16;
+      const int jj = r % C::q, n1 = 16 * (jj >> 1) + 2 * (r / C::q) + (jj & 1), n2 = n1 + 8;
+      uint8_t* p1 = dst + (n1 >> 3) * (D * 8) + (n1 & 7) * 16 + at;
+      uint8_t* p2 = dst + (n2 >> 3) * (D * 8) + (n2 & 7) * 16 + at;
+      if constexpr (kE == 4) {
+        *reinterpret_cast<uint32_t*>(p1) = c1;
+        *reinterpret_cast<uint32_t*>(p2) = c2;
+      } else {
+        *reinterpret_cast<uint16_t*>(p1) = (uint16_t)c1;
+        *reinterpret_cast<uint16_t*>(p2) = (uint16_t)c2;
+      }
+      if (lane == 0) sh.fac[pb][r] = c8_pow2(ex) * (kLog2e / sqrtf((float)D));
+    }
+  }
+  tc::fence_proxy_async();
+}
+
 template <int D, int NR, bool W>
 __global__ void __launch_bounds__(kThreads, 1)
     cache8_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
@@ -289,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(&sh.p_full[i], 128);
       tc::mbar_init(&sh.o_full[i], 1);
       tc::mbar_init(&sh.o_empty[i], 4);
-      tc::mbar_init(&sh.q_full[i], 96);
+      tc::mbar_init(&sh.q_full[i], 32);
       tc::mbar_init(&sh.q_empty[i], 1 + 8);
       sh.nan_any[i] = 0;
     }
@@ -342,9 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort = &sh.abort_flag;
   Walk w;
   walk_begin(w, a, sh.start_b, sh.start_off, t1 - t0);
-  const int R = a.Hq / a.G, rows = a.n_new * R;
-  const long units = (long)a.batch * units_b;
-  const Part<D, NR> part(a.part, units);
+  const Part<D, NR> part(a.part, (long)a.batch * units_b);
 
   if (warp == 0) {
     // ---- TMA: K and V tiles; a lane per block: their scales ----
@@ -354,23 +433,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool mine = j < per && !(W && part_v);
     int k = 0, st = 0;
     uint32_t ph = 1;
-    for (; w.left > 0; walk_next(w, a), ++k) {
-      if (k >= C::kStages) warp_wait(&sh.empty[st], ph, abort, a.status);
-      if (__any_sync(0xFFFFFFFFu, *abort)) break;
-      const int g = w.g;
-      if (lane == 0) {
-        uint8_t* dst = sKV + st * C::kStage;
-        const int z = w.b * a.T + w.tile * kTok;
-        tc::mbar_arrive_expect_tx(&sh.full[st], C::kStage);
-        tc::tma_load_3d(dst, &map_k, &sh.full[st], 0, g, z);
-        if (!W) tc::tma_load_3d(dst + C::kTile, &map_v, &sh.full[st], 0, g, z);
-      }
-      const long blk = (long)w.tile * per + j;
-      if (mine && blk < nblk) cp_async4(&sh.scale[st][lane], scales + ((long)w.b * nblk + blk) * a.G + g);
-      cp_async_arrive(&sh.full[st]);
-      if (++st == C::kStages) {
-        st = 0;
-        ph ^= 1;
+    bool stop = false;
+    for (; w.left > 0 && !stop; walk_next(w, a)) {
+      const float* src = scales + ((long)w.b * nblk + j) * a.G + w.g;
+      const int z = w.b * a.T;
+      for (int tile = w.t0; tile < w.t1; ++tile, ++k) {
+        if (k >= C::kStages) warp_wait(&sh.empty[st], ph, abort, a.status);
+        if ((stop = __any_sync(0xFFFFFFFFu, *abort))) break;
+        if (lane == 0) {
+          uint8_t* dst = sKV + st * C::kStage;
+          tc::mbar_arrive_expect_tx(&sh.full[st], C::kStage);
+          tc::tma_load_3d(dst, &map_k, &sh.full[st], 0, w.g, z + tile * kTok);
+          if (!W) tc::tma_load_3d(dst + C::kTile, &map_v, &sh.full[st], 0, w.g, z + tile * kTok);
+        }
+        const long blk = (long)tile * per;
+        if (mine && blk + j < nblk) cp_async4(&sh.scale[st][lane], src + blk * a.G);
+        cp_async_arrive(&sh.full[st]);
+        if (++st == C::kStages) {
+          st = 0;
+          ph ^= 1;
+        }
       }
     }
     // copies in flight land before the CTA leaves (all have, unless a wait ran out)
@@ -386,27 +468,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t id_s = idesc_f8(C::N, false, false);
       const uint64_t dk = tc::smem_desc_kmajor(sKV, D), dq = tc::smem_desc_kmajor_noswz(sQ, 128, D * 8);
       volatile int none = 0;
-      int k = 0, st = 0, ph = 0;
+      int k = 0, st = 0;
+      uint32_t ph = 0, sph = 0;  // phases of the stages and of S^T's buffers
       bool ok = true;
-      for (; w.left > 0; walk_next(w, a), ++k) {
-        const int sb = k & 1, pb = w.piece & 1;
-        if ((w.first && !tc::mbar_wait(&sh.q_full[pb], (uint32_t)((w.piece >> 1) & 1), abort, a.status)) ||
-            !tc::mbar_wait(&sh.full[st], (uint32_t)ph, abort, a.status) ||
-            (k >= 2 && !tc::mbar_wait(&sh.s_empty[sb], (uint32_t)(((k >> 1) - 1) & 1), abort, a.status))) {
-          ok = false;
-          break;
-        }
-        tc::fence_after_sync();
-        const uint64_t da = dk + (uint32_t)(st * (C::kStage >> 4)), db = dq + (uint32_t)(pb * (C::kQ >> 4));
+      for (; w.left > 0 && ok; walk_next(w, a)) {
+        const int pb = w.piece & 1;
+        const uint64_t db = dq + (uint32_t)(pb * (C::kQ >> 4));
+        ok = tc::mbar_wait(&sh.q_full[pb], (uint32_t)((w.piece >> 1) & 1), abort, a.status);
+        for (int n = w.t1 - w.t0; n > 0 && ok; --n, ++k) {
+          const int sb = k & 1;
+          if (!tc::mbar_wait(&sh.full[st], ph, abort, a.status) ||
+              (k >= 2 && !tc::mbar_wait(&sh.s_empty[sb], sph ^ 1u, abort, a.status))) {
+            ok = false;
+            break;
+          }
+          tc::fence_after_sync();
+          const uint64_t da = dk + (uint32_t)(st * (C::kStage >> 4));
 #pragma unroll
-        for (int kk = 0; kk < D / 32; ++kk)
-          mma_f8(tmem + (uint32_t)(sb * C::N), da + kk * 2, db + kk * 16, id_s, kk > 0);
-        tc::mma_commit(&sh.s_full[sb]);
-        if (W) tc::mma_commit(&sh.empty[st]);
-        if (walk_last(w)) tc::mma_commit(&sh.q_empty[pb]);
-        if (++st == C::kStages) {
-          st = 0;
-          ph ^= 1;
+          for (int kk = 0; kk < D / 32; ++kk)
+            mma_f8(tmem + (uint32_t)(sb * C::N), da + kk * 2, db + kk * 16, id_s, kk > 0);
+          tc::mma_commit(&sh.s_full[sb]);
+          if (W) tc::mma_commit(&sh.empty[st]);
+          if (n == 1) tc::mma_commit(&sh.q_empty[pb]);
+          sph ^= (uint32_t)sb;
+          if (++st == C::kStages) {
+            st = 0;
+            ph ^= 1;
+          }
         }
       }
       if (!ok) {
@@ -418,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (W && ok)
         for (int j = max(0, k - C::kStages); j < k; ++j)
           tc::mbar_wait(&sh.empty[j % C::kStages], (uint32_t)((j / C::kStages) & 1), abort);
-      if (ok) tc::mbar_wait(&sh.q_empty[w.piece & 1], (uint32_t)((w.piece >> 1) & 1), abort);
+      if (ok) tc::mbar_wait(&sh.q_empty[(w.piece - 1) & 1], (uint32_t)(((w.piece - 1) >> 1) & 1), abort);
     }
   } else if (warp == 2) {
     // ---- MMAs of O^T ----
@@ -452,72 +540,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = max(0, k - C::kStages); j < k; ++j)
         tc::mbar_wait(&sh.empty[j % C::kStages], (uint32_t)((j / C::kStages) & 1), &none);
     }
-  } else if (warp == 3 || warp >= 16) {
-    // ---- a unit's rows of q as two E4M3 terms; a warp per row ----
-    constexpr int kE = D / 32;
+  } else if (warp == 3) {
+    // ---- rows of q (the first piece's with the accumulating warps) ----
     for (; w.left > 0; walk_next(w, a)) {
-      if (!w.first) continue;
-      const int pb = w.piece & 1, g = w.g, r0 = w.ch * a.chunk_rows;
+      const int pb = w.piece & 1;
       if (w.piece >= 2) warp_wait(&sh.q_empty[pb], (uint32_t)(((w.piece >> 1) - 1) & 1), abort, a.status);
-      uint8_t* dst = sQ + pb * C::kQ;
-#pragma unroll 4
-      for (int r = warp == 3 ? 0 : warp - 15; r < NR; r += 3) {
-        const int gr = r0 + r;
-        const bool real = r < a.chunk_rows && gr < rows;
-        uint32_t x[kE / 2];
-#pragma unroll
-        for (int e = 0; e < kE / 2; ++e) x[e] = 0u;
-        if (real) {
-          const long src = (((long)w.b * a.n_new + gr / R) * a.Hq + (long)g * R + gr % R) * D + lane * kE;
-          if constexpr (kE == 4) {
-            const uint2 y = __ldg(reinterpret_cast<const uint2*>(a.q + src));
-            x[0] = y.x;
-            x[1] = y.y;
-          } else {
-            x[0] = __ldg(reinterpret_cast<const uint32_t*>(a.q + src));
-          }
-        }
-        uint32_t amax = 0u;
-#pragma unroll
-        for (int e = 0; e < kE / 2; ++e) {
-          const uint32_t lo = x[e] & 0x7FFFu, hi = (x[e] >> 16) & 0x7FFFu;
-          amax = max(amax, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
-        }
-        amax = __reduce_max_sync(0xFFFFFFFFu, amax);
-        const int ex = c8_exponent(amax << 16);
-        const float inv = c8_pow2(-ex);
-        uint32_t c1 = 0u, c2 = 0u;
-#pragma unroll
-        for (int e = 0; e < kE / 2; ++e) {
-          const float y0 = bf16_lo(x[e]) * inv, y1 = bf16_hi(x[e]) * inv;
-          // an infinity becomes NaN, as which it would end in the scores
-          uint32_t t1 = c8_encode2(y0, y1);
-          const float2 f = c8_decode2(t1);
-          uint32_t t2 = c8_encode2((y0 - f.x) * 16.f, (y1 - f.y) * 16.f);
-          if ((x[e] & 0x7F80u) == 0x7F80u) t1 |= 0x7Fu;
-          if ((x[e] & 0x7F800000u) == 0x7F800000u) t1 |= 0x7F00u;
-          c1 |= t1 << (16 * e);
-          c2 |= t2 << (16 * e);
-        }
-        const int at = (lane * kE / 16) * 128 + lane * kE % 16;
-        // columns 8 j + 2 i + x of S^T: row i q + (j / 2) 2 + x, term j % 2
-        const int jj = r % C::q, n1 = 16 * (jj >> 1) + 2 * (r / C::q) + (jj & 1), n2 = n1 + 8;
-        uint8_t* p1 = dst + (n1 >> 3) * (D * 8) + (n1 & 7) * 16 + at;
-        uint8_t* p2 = dst + (n2 >> 3) * (D * 8) + (n2 & 7) * 16 + at;
-        if constexpr (kE == 4) {
-          *reinterpret_cast<uint32_t*>(p1) = c1;
-          *reinterpret_cast<uint32_t*>(p2) = c2;
-        } else {
-          *reinterpret_cast<uint16_t*>(p1) = (uint16_t)c1;
-          *reinterpret_cast<uint16_t*>(p2) = (uint16_t)c2;
-        }
-        if (lane == 0) {
-          sh.fac[pb][r] = c8_pow2(ex) * (kLog2e / sqrtf((float)D));
-          sh.lim[pb][r] = real ? w.L - a.n_new + gr / R : -1;
-          if (W) sh.lse[pb][r] = real ? a.lse[((long)w.b * a.G + g) * rows + gr] : INFINITY;  // no row: 2^-inf
-        }
+      if (w.piece == 0) {
+        split_q<D, NR, W>(a, w, sh, sQ, 0, 5, lane);
+        asm volatile("bar.sync 4, 160;" ::: "memory");
+      } else {
+        split_q<D, NR, W>(a, w, sh, sQ, 0, 1, lane);
       }
-      tc::fence_proxy_async();
       tc::mbar_arrive(&sh.q_full[pb]);
     }
   } else if (warp < 12) {
@@ -529,26 +562,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t fac[q / 2];
 #pragma unroll
     for (int j = 0; j < q / 2; ++j) fac[j] = 0ull;
-    int k = 0, st = 0;
-    uint32_t ph = 0;
-    for (; w.left > 0; walk_next(w, a), ++k) {
+    // tiles k = wg, wg + 2, ..: stage k mod the stages, phase of the buffers k / 2
+    int st = wg;
+    uint32_t ph = 0, kp = 0;
+    for (; w.left > 0; walk_next(w, a)) {
       const int pb = w.piece & 1;
-      if (w.first) {
-        warp_wait(&sh.q_full[pb], (uint32_t)((w.piece >> 1) & 1), abort, a.status);
+      warp_wait(&sh.q_full[pb], (uint32_t)((w.piece >> 1) & 1), abort, a.status);
 #pragma unroll
-        for (int j = 0; j < q / 2; ++j) fac[j] = pack2(sh.fac[pb][row0 + 2 * j], sh.fac[pb][row0 + 2 * j + 1]);
-      }
-      if ((k & 1) == wg) {
-        const int u0 = w.tile * kTok + tok;
-        const int vis = w.L - a.n_new;               // tokens up to here are visible to every row
-        const bool edge = (w.tile + 1) * kTok - 1 > vis;
-        const int uw = w.tile * kTok + q4 * 32 + (lane >> 2) + 8 * i;  // the token whose weight this lane writes
-        const long wi = ((long)w.b * a.G + w.g) * a.T + uw;
+      for (int j = 0; j < q / 2; ++j) fac[j] = pack2(sh.fac[pb][row0 + 2 * j], sh.fac[pb][row0 + 2 * j + 1]);
+      const int vis = w.L - a.n_new;  // tokens up to here are visible to every row
+      const long wi0 = ((long)w.b * a.G + w.g) * a.T;
+      for (int tile = w.t0 + ((w.k ^ wg) & 1); tile < w.t1; tile += 2, ++kp) {
+        const int u0 = tile * kTok + tok;
+        const bool edge = (tile + 1) * kTok - 1 > vis;
+        const int uw = tile * kTok + q4 * 32 + (lane >> 2) + 8 * i;  // the token whose weight this lane writes
+        const long wi = wi0 + uw;
         float sum = 0.f;
         if constexpr (W) {
           if (a.w_in && uw < vis) sum = a.w_in[wi];
         }
-        warp_wait(&sh.s_full[wg], (uint32_t)((k >> 1) & 1), abort, a.status);
+        warp_wait(&sh.s_full[wg], kp & 1u, abort, a.status);
         warp_wait(&sh.full[st], ph, abort, a.status);
         tc::fence_after_sync();
         float sk[4];
@@ -642,14 +675,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float mine = across_tokens<q>(mx, lane, [](float x, float y) { return fmaxf(x, y); });
           we = __reduce_max_sync(0xFFFFFFFFu, we);
           // the P buffer and the numbers of the tile two tiles back have been read
-          if (k >= 2) warp_wait(&sh.o_empty[wg], (uint32_t)(((k >> 1) - 1) & 1), abort, a.status);
+          if (kp > 0) warp_wait(&sh.o_empty[wg], (kp & 1u) ^ 1u, abort, a.status);
           if ((lane >> 2) < q) sh.wmax[wg][q4][row0 + (lane >> 2)] = mine;
           if (lane == 0) sh.wev[wg][q4] = we;
           if (edge) {
             // A zero probability must not meet a NaN code: rows behind the last token become zeros,
             // and a NaN of a token that some row does not see is noted and taken out; the rows that
             // see it get it back at the end.
-            const int u = w.tile * kTok + t;
+            const int u = tile * kTok + t;
             uint8_t* v = sKV + st * C::kStage + C::kTile + t * D;
             if (u >= w.L) {
 #pragma unroll
@@ -722,17 +755,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           if ((lane >> 2) < q) sh.wsum_p[wg][q4][row0 + (lane >> 2)] = s;
           tc::mbar_arrive(&sh.p_full[wg]);
         }
+        st += 2;
+        if (st >= C::kStages) {
+          st -= C::kStages;
+          ph ^= 1;
+        }
       }
-      if (walk_last(w)) {
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sh.q_empty[pb]);
-      }
-      if (++st == C::kStages) {
-        st = 0;
-        ph ^= 1;
-      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sh.q_empty[pb]);
     }
-  } else if (!W) {
+  } else {
+    split_q<D, NR, W>(a, w, sh, sQ, warp - 11, 5, lane);
+    asm volatile("bar.arrive 4, 160;" ::: "memory");
+    if constexpr (!W) {
     // ---- a thread per head dim: outputs ----
     const int q4 = warp & 3, t = tid & 127;
     const int dim = D == 128 ? t : t & 63, rb = D == 128 ? 0 : (t >> 6) * C::kRowsT;
@@ -743,11 +778,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int r = 0; r < C::kRowsT / 2; ++r) o[r] = 0ull;
     float m_run = kNegMax, l = 0.f;  // row t's, in the first threads
     int e_run = -126;
-    int first_tile = 0;
     int k = 0;
-    for (; w.left > 0; walk_next(w, a), ++k) {
-      const int pb = w.piece & 1, sb = k & 1;
-      if (w.first) first_tile = w.tile;
+    for (; w.left > 0; walk_next(w, a)) {
+     const int pb = w.piece & 1;
+     const long unit = (long)w.b * units_b + w.g * a.nch + w.ch, slot = unit + blockIdx.x;
+     for (int n = w.t1 - w.t0; n > 0; --n, ++k) {
+      const int sb = k & 1;
       warp_wait(&sh.p_full[sb], (uint32_t)((k >> 1) & 1), abort, a.status);
       const int et = max(max(sh.wev[sb][0], sh.wev[sb][1]), max(sh.wev[sb][2], sh.wev[sb][3])), en = max(e_run, et);
       if (t < NR) {
@@ -790,11 +826,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tc::fence_before_sync();
-      const bool last = walk_last(w);
-      const long unit = (long)w.b * units_b + w.g * a.nch + w.ch, slot = unit + blockIdx.x;
-      if (last) {
+      if (n == 1) {
         if (sh.nan_any[pb]) {
-          const int np = sh.nan_at[pb][dim], r0 = w.ch * a.chunk_rows + rb;
+          const int np = sh.nan_at[pb][dim], r0 = w.ch * a.chunk_rows + rb, R = a.Hq / a.G;
 #pragma unroll
           for (int r = 0; r < C::kRowsT; r += 2) {
             const float nan = __int_as_float(0x7FC00000);
@@ -809,7 +843,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sh.o_empty[sb]);
-      if (last) {
+     }
         float* po = part.o(slot) + rb * D + dim;
 #pragma unroll
         for (int r = 0; r < C::kRowsT; r += 2) {
@@ -824,13 +858,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (t == 0) {
           *part.e(slot) = e_run;
-          if (first_tile == 0) part.first[unit] = (int)blockIdx.x;
-          if (w.tile + 1 == w.ntiles) part.last[unit] = (int)blockIdx.x;
+          if (w.t0 == 0) part.first[unit] = (int)blockIdx.x;
+          if (w.t1 == w.ntiles) part.last[unit] = (int)blockIdx.x;
         }
         m_run = kNegMax;
         l = 0.f;
         e_run = -126;
-      }
+    }
     }
   }
   tc::fence_before_sync();
