@@ -1,11 +1,13 @@
 // Appending tokens to the block-scaled 8-bit KV cache (format: cache8.cuh).
 //
 // A work item is one touched block of one (sequence, group), K and V together: every thread loads
-// 16 dims of a row (two 16-byte loads of bf16 for K, two for V), the item's largest finite
-// magnitudes meet in shared memory, and the codes go out as one 16-byte store per row piece: each
-// new element is read once and written once, no second pass. A block that held tokens before keeps
-// its scale unless a new token needs a larger one; only then are its codes read, rounded again and
-// rewritten. HBM bound: 2 bytes read and 1 written per element.
+// 16 dims of a row (32 bytes of bf16 for K, 32 for V), the item's largest finite magnitudes meet in
+// shared memory, and the codes go out as one 16-byte store per row piece: each new element is read
+// once and written once, no second pass. A block that held tokens before keeps its scale unless a new
+// token needs a larger one; only then are its codes read, rounded again and rewritten. HBM bound: 2
+// bytes read and 1 written per element. (Item indices are 32-bit and the sequence is a grid
+// dimension: with 64-bit divisions the kernel was bound by them, 106 us for 8 prompts of up to 24K
+// tokens, 258 MB.)
 #include "cache8.cuh"
 
 namespace sgqa {
@@ -13,15 +15,19 @@ namespace {
 
 constexpr int kThr = 256;
 
-// Largest finite magnitude (bf16 bits) of eight bf16 values.
-__device__ __forceinline__ uint32_t amax8(const uint4& x) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+// Largest finite magnitude (bf16 bits) of 16 bf16 values.
+__device__ __forceinline__ uint32_t amax16(const uint4 (&x)[2]) {
+  const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+  m = max(m & 0xFFFFu, m >> 16);
+  if (m < 0x7F80u) return m;
+  m = 0;  // an infinity or NaN among them
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
     const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
-    if (lo < 0x7F80u) m = max(m, lo);
-    if (hi < 0x7F80u) m = max(m, hi);
+    m = max(m, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
   }
   return m;
 }
@@ -36,7 +42,7 @@ __device__ __forceinline__ uint2 encode8(const uint4& x, float inv) {
 // D: head dim; BLK: tokens per block. Rows of a block are spread over the threads, D / 16 to a row;
 // small blocks share a CTA (a warp always serves one item), large ones take several passes.
 template <int D, int BLK>
-__global__ void __launch_bounds__(kThr) cache8_append_kernel(C8AppendArgs a, int blocks_per_seq) {
+__global__ void __launch_bounds__(kThr) cache8_append_kernel(C8AppendArgs a, int items) {
   constexpr int kTpr = D / 16, kRows = kThr / kTpr;
   constexpr int kItems = kRows > BLK ? kRows / BLK : 1;
   constexpr int kPass = BLK > kRows ? BLK / kRows : 1;
@@ -47,11 +53,9 @@ __global__ void __launch_bounds__(kThr) cache8_append_kernel(C8AppendArgs a, int
   const int sub = kItems > 1 ? (tid / kTpr) / BLK : 0;
   const int row0 = kItems > 1 ? (tid / kTpr) % BLK : tid / kTpr;
   const int col = (tid % kTpr) * 16;
-  const long item = (long)blockIdx.x * kItems + sub;  // (b, touched block, g), g fastest
-  const long per_seq = (long)blocks_per_seq * a.G;
-  const int b = (int)(item / per_seq);
-  const int g = (int)(item % a.G);
-  bool live = b < a.batch;
+  const unsigned item = blockIdx.x * kItems + sub;  // (touched block, g) of sequence b, g fastest
+  const int b = blockIdx.y, g = (int)(item % (unsigned)a.G);
+  bool live = item < (unsigned)items;
   int L = 0, end = 0, j = 0;
   if (live) {
     const int cnt = a.counts ? __ldg(a.counts + b) : a.n_t;
@@ -59,7 +63,7 @@ __global__ void __launch_bounds__(kThr) cache8_append_kernel(C8AppendArgs a, int
     live = L >= 0 && cnt >= 0 && cnt <= a.n_t && (long)L + cnt <= a.T;
     if (!live) report(a.status, SGQA_ERR_DEVICE_CHECK);
     end = L + cnt;
-    j = L / BLK + (int)((item % per_seq) / a.G);
+    j = L / BLK + (int)(item / (unsigned)a.G);
     live = live && cnt > 0 && (long)j * BLK < end;
   }
   uint4 xk[kPass][2], xv[kPass][2];
@@ -81,8 +85,8 @@ __global__ void __launch_bounds__(kThr) cache8_append_kernel(C8AppendArgs a, int
   }
 #pragma unroll
   for (int p = 0; p < kPass; ++p) {
-    mk = max(mk, max(amax8(xk[p][0]), amax8(xk[p][1])));
-    mv = max(mv, max(amax8(xv[p][0]), amax8(xv[p][1])));
+    mk = max(mk, amax16(xk[p]));
+    mv = max(mv, amax16(xv[p]));
   }
   mk = __reduce_max_sync(0xFFFFFFFFu, mk);
   mv = __reduce_max_sync(0xFFFFFFFFu, mv);
@@ -138,11 +142,9 @@ cudaError_t launch(const C8AppendArgs& a, cudaStream_t s) {
   // n_t tokens can touch one block more than they fill, but never more than there are
   const long nblk = ((long)a.T + BLK - 1) / BLK;
   const long touched = ((long)a.n_t + BLK - 1) / BLK + 1;
-  const int per_seq = (int)(touched < nblk ? touched : nblk);
-  const long items = (long)a.batch * per_seq * a.G;
-  const long ctas = (items + kItems - 1) / kItems;
-  if (ctas > 0x7FFFFFFFL) return cudaErrorInvalidConfiguration;
-  cache8_append_kernel<D, BLK><<<(unsigned)ctas, kThr, 0, s>>>(a, per_seq);
+  const long items = (touched < nblk ? touched : nblk) * a.G;  // of a sequence; T * G is below 2^31
+  const unsigned ctas = (unsigned)((items + kItems - 1) / kItems);
+  cache8_append_kernel<D, BLK><<<dim3(ctas, (unsigned)a.batch), kThr, 0, s>>>(a, (int)items);
   return cudaGetLastError();
 }
 template <int D>
