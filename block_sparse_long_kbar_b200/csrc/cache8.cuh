@@ -96,6 +96,13 @@ __device__ __forceinline__ uint32_t c8_rescale4(uint32_t w, float f) {
 // 2^k for rescaling codes; beyond +-40 every code but 0 saturates or vanishes anyway
 __device__ __forceinline__ float c8_shift(int k) { return c8_pow2(max(-40, min(40, k))); }
 
+// the larger of each 16-bit half
+__device__ __forceinline__ uint32_t c8_max_u16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+
 // lens[b] if it is a length this cache can have, else 0 and a device check
 __device__ __forceinline__ int c8_len(const int32_t* lens, int b, int T, int* status) {
   const int n = __ldg(lens + b);

@@ -103,6 +103,7 @@ int sgqa_cache8_evict(const sgqa_dims* dims, int block, const int32_t* lens, int
   const int rc = check_cache8(dims, block);
   if (rc) return rc;
   if (keep <= 0 || recent < 0 || recent > keep || T_out < keep || T_out >= (1 << 28)) return SGQA_ERR_INVALID_ARG;
+  if ((long)dims->batch * T_out * dims->G >= (1L << 31)) return SGQA_ERR_UNSUPPORTED;  // row indices are 32-bit
   if (!aligned16(lens) || !aligned16(weight) || !cache_ok(k8, k_scale, v8, v_scale) ||
       !cache_ok(k8_out, k_scale_out, v8_out, v_scale_out) || !aligned16(weight_out) || !aligned16(kept) ||
       !aligned16(lens_out))

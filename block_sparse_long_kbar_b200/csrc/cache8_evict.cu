@@ -196,7 +196,7 @@ __device__ __forceinline__ uint32_t amax16(const uint4& x, float scale) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   uint32_t m = 0;  // the largest magnitude code that is no NaN
 #pragma unroll
-  for (int i = 0; i < 4; ++i) m = __vmaxu2(m, __vmaxu2(w[i] & 0x007F007Fu, (w[i] >> 8) & 0x007F007Fu));
+  for (int i = 0; i < 4; ++i) m = c8_max_u16x2(m, c8_max_u16x2(w[i] & 0x007F007Fu, (w[i] >> 8) & 0x007F007Fu));
   m = max(m & 0xFFFFu, m >> 16);
   if (m == 0x7Fu) {
     m = 0;
@@ -213,69 +213,79 @@ __device__ __forceinline__ uint4 rescale16(const uint4& x, int k) {
   return make_uint4(c8_rescale4(x.x, f), c8_rescale4(x.y, f), c8_rescale4(x.z, f), c8_rescale4(x.w, f));
 }
 
-// One item per block of the new cache and group, rows as in the append kernel. HBM bound: a kept row
-// is read and written once.
+// One item per block of the new cache and group, rows and items as in the append kernel. HBM bound: a
+// kept row is read and written once.
+constexpr int kLoop = 8;
 template <int D, int BLK>
-__global__ void __launch_bounds__(kThr) cache8_move_kernel(C8EvictArgs a, int items) {
+__global__ void __launch_bounds__(kThr) cache8_move_kernel(C8EvictArgs a, int loop) {
   constexpr int kTpr = D / 16, kRows = kThr / kTpr;
   constexpr int kItems = kRows > BLK ? kRows / BLK : 1;
   constexpr int kPass = BLK > kRows ? BLK / kRows : 1;
-  __shared__ uint32_t amax[kItems][2];
-  const int tid = threadIdx.x;
-  if (tid < kItems * 2) amax[tid / 2][tid & 1] = 0u;
+  __shared__ uint32_t amax[kLoop][kItems][2];
+  const int tid = threadIdx.x, b = blockIdx.y;
+  const int m = min(c8_len(a.lens, b, a.T, a.status), a.keep);
+  const int first = (int)blockIdx.x * loop * kItems;
+  if (first / a.G * BLK >= m) return;
+  for (int i = tid; i < kLoop * kItems * 2; i += kThr) (&amax[0][0][0])[i] = 0u;
   __syncthreads();
   const int sub = kItems > 1 ? (tid / kTpr) / BLK : 0;
   const int row0 = kItems > 1 ? (tid / kTpr) % BLK : tid / kTpr;
   const int col = (tid % kTpr) * 16;
-  const unsigned item = blockIdx.x * kItems + sub;  // (block, g) of sequence b, g fastest
-  const int b = blockIdx.y, g = (int)(item % (unsigned)a.G), j = (int)(item / (unsigned)a.G);
-  int m = 0;
-  if (item < (unsigned)items) m = min(c8_len(a.lens, b, a.T, a.status), a.keep);
-  const long nblk = (a.T + BLK - 1) / BLK, nblk_out = (a.T_out + BLK - 1) / BLK;
-  uint4 xk[kPass], xv[kPass];
-  int ek[kPass], ev[kPass];
-  uint32_t mk = 0, mv = 0;
+  const int nblk = (a.T + BLK - 1) / BLK, nblk_out = (a.T_out + BLK - 1) / BLK;
+  int j = (first + sub) / a.G, g = (first + sub) % a.G;
+  for (int it = 0; it < loop; ++it) {
+    uint4 xk[kPass], xv[kPass];
+    int ek[kPass], ev[kPass], u[kPass];
+    uint32_t mk = 0, mv = 0;
+    const int i0 = j * BLK + row0;
 #pragma unroll
-  for (int p = 0; p < kPass; ++p) {
-    const int i = j * BLK + row0 + p * kRows;
-    xk[p] = xv[p] = make_uint4(0, 0, 0, 0);
-    ek[p] = ev[p] = -126;
-    if (i < m) {
-      const int u = __ldg(a.kept + ((long)b * a.G + g) * a.keep + i);
-      const long src = (((long)b * a.T + u) * a.G + g) * D + col;
-      const long si = ((long)b * nblk + u / BLK) * a.G + g;
-      xk[p] = __ldg(reinterpret_cast<const uint4*>(a.src.k8 + src));
-      xv[p] = __ldg(reinterpret_cast<const uint4*>(a.src.v8 + src));
-      ek[p] = c8_scale_exponent(__ldg(a.src.ks + si));
-      ev[p] = c8_scale_exponent(__ldg(a.src.vs + si));
-      if (col == 0) a.w_out[((long)b * a.G + g) * a.T_out + i] = __ldg(a.weight + ((long)b * a.G + g) * a.T + u);
+    for (int p = 0; p < kPass; ++p)
+      u[p] = i0 + p * kRows < m ? __ldg(a.kept + (long)(b * a.G + g) * a.keep + i0 + p * kRows) : -1;
+#pragma unroll
+    for (int p = 0; p < kPass; ++p) {
+      xk[p] = xv[p] = make_uint4(0, 0, 0, 0);
+      ek[p] = ev[p] = -126;
+      if (u[p] >= 0) {
+        const long src = (long)((b * a.T + u[p]) * a.G + g) * D + col;
+        const long si = (long)(b * nblk + u[p] / BLK) * a.G + g;
+        xk[p] = __ldg(reinterpret_cast<const uint4*>(a.src.k8 + src));
+        xv[p] = __ldg(reinterpret_cast<const uint4*>(a.src.v8 + src));
+        ek[p] = c8_scale_exponent(__ldg(a.src.ks + si));
+        ev[p] = c8_scale_exponent(__ldg(a.src.vs + si));
+      }
     }
-  }
+    if (col == 0) {
 #pragma unroll
-  for (int p = 0; p < kPass; ++p) {
-    mk = max(mk, amax16(xk[p], c8_pow2(ek[p])));
-    mv = max(mv, amax16(xv[p], c8_pow2(ev[p])));
-  }
-  mk = __reduce_max_sync(0xFFFFFFFFu, mk);
-  mv = __reduce_max_sync(0xFFFFFFFFu, mv);
-  if ((tid & 31) == 0) {
-    atomicMax(&amax[sub][0], mk);
-    atomicMax(&amax[sub][1], mv);
-  }
-  __syncthreads();
-  const int nk = c8_exponent(amax[sub][0]), nv = c8_exponent(amax[sub][1]);
+      for (int p = 0; p < kPass; ++p)
+        if (u[p] >= 0)
+          a.w_out[(long)(b * a.G + g) * a.T_out + i0 + p * kRows] = __ldg(a.weight + (long)(b * a.G + g) * a.T + u[p]);
+    }
 #pragma unroll
-  for (int p = 0; p < kPass; ++p) {
-    const int i = j * BLK + row0 + p * kRows;
-    if (i >= m) break;
-    const long dst = (((long)b * a.T_out + i) * a.G + g) * D + col;
-    *reinterpret_cast<uint4*>(a.dst.k8 + dst) = rescale16(xk[p], ek[p] - nk);
-    *reinterpret_cast<uint4*>(a.dst.v8 + dst) = rescale16(xv[p], ev[p] - nv);
-  }
-  if (row0 == 0 && col == 0 && j * BLK < m) {
-    const long so = ((long)b * nblk_out + j) * a.G + g;
-    a.dst.ks[so] = c8_pow2(nk);
-    a.dst.vs[so] = c8_pow2(nv);
+    for (int p = 0; p < kPass; ++p) {
+      mk = max(mk, amax16(xk[p], c8_pow2(ek[p])));
+      mv = max(mv, amax16(xv[p], c8_pow2(ev[p])));
+    }
+    mk = __reduce_max_sync(0xFFFFFFFFu, mk);
+    mv = __reduce_max_sync(0xFFFFFFFFu, mv);
+    if ((tid & 31) == 0) {
+      atomicMax(&amax[it][sub][0], mk);
+      atomicMax(&amax[it][sub][1], mv);
+    }
+    __syncthreads();
+    const int nk = c8_exponent(amax[it][sub][0]), nv = c8_exponent(amax[it][sub][1]);
+#pragma unroll
+    for (int p = 0; p < kPass; ++p) {
+      if (u[p] < 0) break;
+      const long dst = (long)((b * a.T_out + i0 + p * kRows) * a.G + g) * D + col;
+      *reinterpret_cast<uint4*>(a.dst.k8 + dst) = rescale16(xk[p], ek[p] - nk);
+      *reinterpret_cast<uint4*>(a.dst.v8 + dst) = rescale16(xv[p], ev[p] - nv);
+    }
+    if (row0 == 0 && col == 0 && u[0] >= 0) {
+      const long so = (long)(b * nblk_out + j) * a.G + g;
+      a.dst.ks[so] = c8_pow2(nk);
+      a.dst.vs[so] = c8_pow2(nv);
+    }
+    for (g += kItems; g >= a.G; g -= a.G) ++j;
   }
 }
 
@@ -285,8 +295,10 @@ cudaError_t launch_move(const C8EvictArgs& a, cudaStream_t s) {
   constexpr int kItems = kRows > BLK ? kRows / BLK : 1;
   const int most = a.keep < a.T ? a.keep : a.T;  // tokens a sequence can keep
   const long items = (long)((most + BLK - 1) / BLK) * a.G;  // of a sequence; T * G is below 2^31
-  const unsigned ctas = (unsigned)((items + kItems - 1) / kItems);
-  cache8_move_kernel<D, BLK><<<dim3(ctas, (unsigned)a.batch), kThr, 0, s>>>(a, (int)items);
+  const long groups = (items + kItems - 1) / kItems, full = groups * a.batch / (148 * 6 * 4);
+  const int loop = (int)(full < 1 ? 1 : full > kLoop ? kLoop : full);
+  cache8_move_kernel<D, BLK><<<dim3((unsigned)((groups + loop - 1) / loop), (unsigned)a.batch), kThr, 0, s>>>(
+      a, loop);
   return cudaGetLastError();
 }
 template <int D>
