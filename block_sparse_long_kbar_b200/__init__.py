@@ -114,16 +114,37 @@ def _ptr(t, name):
         raise ValueError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
+
+
+def _here(ws):
+    """The device of ws, which has to be the current one."""
+    import torch
+    dev = ws.get_device()
+    if dev < 0:
+        raise ValueError("ws must be a CUDA tensor")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"ws is on device {dev}, not on the current one")
+    return dev
+
+
+def _at(t, name, dev):
+    """Address of a contiguous tensor on device dev (None stays None)."""
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on the device of ws")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _stream(stream):
     import torch
     if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-    if isinstance(stream, int):
-        return ctypes.c_void_p(stream)
-    return ctypes.c_void_p(stream.cuda_stream)
+        # (without building a Stream object, which takes some 3 us: as long as a small call's kernels)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _check(fn, rc):
@@ -286,32 +307,35 @@ def sgqa_cache8_workspace_size(dims: sgqa_dims, block: int, n_new: int) -> int:
 
 def sgqa_cache8_append(dims, block, lens, n_t, k_new, v_new, k8, k_scale, v8, v_scale, ws, counts=None, stream=None):
     """Store the first counts[b] (default: all n_t) tokens of k_new, v_new behind the lens[b] cached ones."""
+    dev = _here(ws)
     _check("sgqa_cache8_append", load_library().sgqa_cache8_append(
-        ctypes.byref(dims), int(block), _ptr(lens, "lens"), _ptr(counts, "counts"), int(n_t), _ptr(k_new, "k_new"),
-        _ptr(v_new, "v_new"), _ptr(k8, "k8"), _ptr(k_scale, "k_scale"), _ptr(v8, "v8"), _ptr(v_scale, "v_scale"),
-        _ptr(ws, "ws"), ws.numel(), _stream(stream)))
+        ctypes.byref(dims), int(block), _at(lens, "lens", dev), _at(counts, "counts", dev), int(n_t), _at(k_new, "k_new", dev),
+        _at(v_new, "v_new", dev), _at(k8, "k8", dev), _at(k_scale, "k_scale", dev), _at(v8, "v8", dev), _at(v_scale, "v_scale", dev),
+        _at(ws, "ws", dev), ws.numel(), _stream(stream)))
 
 
 def sgqa_cache8_attend(dims, block, lens, n_new, q, gate, k8, k_scale, v8, v_scale, out, ws, weight_in=None,
                        weight_out=None, stream=None):
     """Dense gated attention of the last n_new of lens[b] tokens over the block-scaled 8-bit cache; with
     weight_out, also the attention weight that every token has received (on top of weight_in)."""
+    dev = _here(ws)
     _check("sgqa_cache8_attend", load_library().sgqa_cache8_attend(
-        ctypes.byref(dims), int(block), _ptr(lens, "lens"), int(n_new), _ptr(q, "q"), _ptr(gate, "gate"),
-        _ptr(k8, "k8"), _ptr(k_scale, "k_scale"), _ptr(v8, "v8"), _ptr(v_scale, "v_scale"), _ptr(out, "out"),
-        _ptr(weight_in, "weight_in"), _ptr(weight_out, "weight_out"), _ptr(ws, "ws"), ws.numel(), _stream(stream)))
+        ctypes.byref(dims), int(block), _at(lens, "lens", dev), int(n_new), _at(q, "q", dev), _at(gate, "gate", dev),
+        _at(k8, "k8", dev), _at(k_scale, "k_scale", dev), _at(v8, "v8", dev), _at(v_scale, "v_scale", dev), _at(out, "out", dev),
+        _at(weight_in, "weight_in", dev), _at(weight_out, "weight_out", dev), _at(ws, "ws", dev), ws.numel(), _stream(stream)))
 
 
 def sgqa_cache8_evict(dims, block, lens, keep, recent, T_out, weight, k8, k_scale, v8, v_scale, k8_out, k_scale_out,
                       v8_out, v_scale_out, weight_out, kept, lens_out, ws, stream=None):
     """Move the `recent` last and the heaviest other tokens, `keep` in all per (sequence, group), to
     another cache of capacity T_out."""
+    dev = _here(ws)
     _check("sgqa_cache8_evict", load_library().sgqa_cache8_evict(
-        ctypes.byref(dims), int(block), _ptr(lens, "lens"), int(keep), int(recent), int(T_out),
-        _ptr(weight, "weight"), _ptr(k8, "k8"), _ptr(k_scale, "k_scale"), _ptr(v8, "v8"), _ptr(v_scale, "v_scale"),
-        _ptr(k8_out, "k8_out"), _ptr(k_scale_out, "k_scale_out"), _ptr(v8_out, "v8_out"),
-        _ptr(v_scale_out, "v_scale_out"), _ptr(weight_out, "weight_out"), _ptr(kept, "kept"),
-        _ptr(lens_out, "lens_out"), _ptr(ws, "ws"), ws.numel(), _stream(stream)))
+        ctypes.byref(dims), int(block), _at(lens, "lens", dev), int(keep), int(recent), int(T_out),
+        _at(weight, "weight", dev), _at(k8, "k8", dev), _at(k_scale, "k_scale", dev), _at(v8, "v8", dev), _at(v_scale, "v_scale", dev),
+        _at(k8_out, "k8_out", dev), _at(k_scale_out, "k_scale_out", dev), _at(v8_out, "v8_out", dev),
+        _at(v_scale_out, "v_scale_out", dev), _at(weight_out, "weight_out", dev), _at(kept, "kept", dev),
+        _at(lens_out, "lens_out", dev), _at(ws, "ws", dev), ws.numel(), _stream(stream)))
 
 
 def sgqa_test_stall_decode_cta(cta: int):

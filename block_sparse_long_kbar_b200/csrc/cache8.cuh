@@ -60,9 +60,11 @@ struct C8EvictArgs {
   float* w_out;         // [batch, G, T_out]
   int32_t* kept;        // [batch, G, keep]
   int32_t* lens_out;
+  uint32_t* grid_ws;  // cache8_keep_bytes
   int batch, T, T_out, G, d, block, keep, recent;
   int* status;
 };
+size_t cache8_keep_bytes(int batch, int G, int T);
 cudaError_t launch_cache8_evict(const C8EvictArgs& a, cudaStream_t s);
 
 // ---- device helpers ----------------------------------------------------------------------------
@@ -88,13 +90,34 @@ __device__ __forceinline__ float2 c8_decode2(uint32_t two) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(two & 0xFFFFu), __NV_E4M3);
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
-// four codes times 2^k, rounded to E4M3 again (one rounding: the products are exact in fp32)
+// four codes times f, rounded to E4M3 again (one rounding: the products are exact in fp32)
 __device__ __forceinline__ uint32_t c8_rescale4(uint32_t w, float f) {
   const float2 a = c8_decode2(w), b = c8_decode2(w >> 16);
   return c8_encode2(a.x * f, a.y * f) | (c8_encode2(b.x * f, b.y * f) << 16);
 }
+// 16 codes times 2^k, rounded to E4M3 again. For k of [-24, 15] in fp16: a product of 2^-11 or more is
+// exact there, one below becomes 0 as it should.
+__device__ __forceinline__ uint32_t c8_rescale2_half(uint32_t two, __half2 f) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(two & 0xFFFFu), __NV_E4M3);
+  const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h), f);
+  return __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&y), __NV_SATFINITE, __NV_E4M3);
+}
 // 2^k for rescaling codes; beyond +-40 every code but 0 saturates or vanishes anyway
 __device__ __forceinline__ float c8_shift(int k) { return c8_pow2(max(-40, min(40, k))); }
+
+__device__ __forceinline__ uint4 c8_rescale16(const uint4& x, int k) {
+  if (k == 0) return x;
+  if (k > 15) {
+    const float f = c8_shift(k);
+    return make_uint4(c8_rescale4(x.x, f), c8_rescale4(x.y, f), c8_rescale4(x.z, f), c8_rescale4(x.w, f));
+  }
+  const __half2 f = __float2half2_rn(c8_pow2(max(-24, k)));
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = c8_rescale2_half(w[i], f) | (c8_rescale2_half(w[i] >> 16, f) << 16);
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
 
 // the larger of each 16-bit half
 __device__ __forceinline__ uint32_t c8_max_u16x2(uint32_t x, uint32_t y) {

@@ -34,6 +34,9 @@ Cache8Ws cache8_layout(const sgqa_dims* d, int n_new, void* ws) {
   return w;
 }
 
+// attention's and eviction's workspaces lie at the same place: no call keeps anything there
+size_t evict_bytes(const sgqa_dims* d) { return kStatusBytes + align256(cache8_keep_bytes(d->batch, d->G, d->T)); }
+
 bool ws_ok(const void* ws, size_t have, size_t need) {
   return ws && (reinterpret_cast<uintptr_t>(ws) & 255u) == 0 && have >= need;
 }
@@ -52,7 +55,8 @@ extern "C" {
 
 size_t sgqa_cache8_workspace_size(const sgqa_dims* dims, int block, int n_new) {
   if (check_cache8(dims, block) != SGQA_OK || n_new <= 0 || (long)n_new * (dims->Hq / dims->G) > kC8MaxRows) return 0;
-  return cache8_layout(dims, n_new, nullptr).bytes;
+  const size_t at = cache8_layout(dims, n_new, nullptr).bytes, ev = evict_bytes(dims);
+  return at > ev ? at : ev;
 }
 
 int sgqa_cache8_append(const sgqa_dims* dims, int block, const int32_t* lens, const int32_t* counts, int n_t,
@@ -109,8 +113,9 @@ int sgqa_cache8_evict(const sgqa_dims* dims, int block, const int32_t* lens, int
       !aligned16(lens_out))
     return SGQA_ERR_INVALID_ARG;
   if (k8_out == k8 || v8_out == v8 || weight_out == weight || lens_out == lens) return SGQA_ERR_INVALID_ARG;
-  if (!ws_ok(ws, ws_bytes, kStatusBytes)) return SGQA_ERR_WORKSPACE;
+  if (!ws_ok(ws, ws_bytes, evict_bytes(dims))) return SGQA_ERR_WORKSPACE;
   C8EvictArgs a{};
+  a.grid_ws = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + kStatusBytes);
   a.lens = lens; a.weight = weight; a.src = cache_of(k8, k_scale, v8, v_scale);
   a.dst = cache_of(k8_out, k_scale_out, v8_out, v_scale_out); a.w_out = weight_out; a.kept = kept;
   a.lens_out = lens_out; a.batch = dims->batch; a.T = dims->T; a.T_out = T_out; a.G = dims->G; a.d = dims->d;

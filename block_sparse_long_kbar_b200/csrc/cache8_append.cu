@@ -117,16 +117,8 @@ __global__ void __launch_bounds__(kThr) cache8_append_kernel(C8AppendArgs a, int
           *ok = make_uint4(k0.x, k0.y, k1.x, k1.y);
           *ov = make_uint4(v0.x, v0.y, v1.x, v1.y);
         } else {
-          if (ek > ek_old) {
-            const float f = c8_shift(ek_old - ek);
-            const uint4 w = *ok;
-            *ok = make_uint4(c8_rescale4(w.x, f), c8_rescale4(w.y, f), c8_rescale4(w.z, f), c8_rescale4(w.w, f));
-          }
-          if (ev > ev_old) {
-            const float f = c8_shift(ev_old - ev);
-            const uint4 w = *ov;
-            *ov = make_uint4(c8_rescale4(w.x, f), c8_rescale4(w.y, f), c8_rescale4(w.z, f), c8_rescale4(w.w, f));
-          }
+          if (ek > ek_old) *ok = c8_rescale16(*ok, ek_old - ek);
+          if (ev > ev_old) *ov = c8_rescale16(*ov, ev_old - ev);
         }
       }
       if (row0 == 0 && col == 0) {

@@ -10,9 +10,10 @@ namespace sgqa {
 namespace {
 
 constexpr int kSelThr = 1024;
-constexpr int kSelVec = 4;                       // 16-byte loads a lane keeps in flight (or in registers)
-constexpr int kSelWarp = kSelVec * 32;           // and a warp: 512 weights
-constexpr int kSelCta = kSelWarp * 4 * 32;       // weights a CTA can hold in registers: 16384
+constexpr int kSelPart = 4 * kSelThr;  // weights of a CTA per 16-byte load of its threads
+
+// Words of global memory that the selection over the whole GPU has per unit.
+__device__ __host__ constexpr long keep_grid_words(int ctas) { return 3 * 2048 + 8 + 2L * ((ctas + 1) & ~1); }
 
 // Order-preserving key of a weight; NaN ranks as -infinity. No weight's key is 0.
 __device__ __forceinline__ uint32_t weight_key(float w) { return score_key(w != w ? -INFINITY : w); }
@@ -40,129 +41,72 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* buf, uint32
   return before + y - x;
 }
 
-// Of more than `keep` tokens the `recent` last stay, and of the N before them the c = keep - recent
-// heaviest: a radix select (11, 11 and 10 bits) finds the key of the c-th heaviest and how many of its
-// equals stay, the lowest positions first; an ordered pass writes the positions. A cluster of CTAs
-// serves one (sequence, group): each histograms its part of the weights (a contiguous range, split
-// into one per warp) in its own shared memory and adds up the others' over distributed shared memory.
-// REG: a part fits the CTA's registers and is read once; else it is read in every pass (from L2).
-template <bool REG>
-__global__ void __launch_bounds__(kSelThr) cache8_keep_kernel(C8EvictArgs a) {
-  __shared__ alignas(16) uint32_t hist[3][2048];
-  __shared__ uint32_t buf[32], s_bin, s_need, s_count[2];
-  const cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
-  const int unit = blockIdx.x / ctas, b = unit / a.G, g = unit % a.G;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int L = c8_len(a.lens, b, a.T, a.status);
-  const int m = min(L, a.keep);
-  int32_t* kept = a.kept + (long)unit * a.keep;
-  const int t = rank * kSelThr + tid, step = ctas * kSelThr;
-  if (g == 0 && t == 0) a.lens_out[b] = m;
-  for (int i = m + t; i < a.keep; i += step) kept[i] = -1;
-  if (L <= a.keep) {
-    for (int i = t; i < L; i += step) kept[i] = i;
-    return;
+// The weights of one (sequence, group) that compete, and the part of them that one warp takes: 16-byte
+// aligned vectors v0 .. v1 - 1, vector v holding weights 4 v - off ..; VEC vectors of a lane at a time.
+template <int VEC>
+struct Part {
+  const float* w;
+  int off, N, v0, v1;
+  uint32_t key[VEC][4];
+  float4 ahead[VEC];
+  __device__ __forceinline__ void set(const C8EvictArgs& a, int unit, int n, int ctas, int rank, int warps) {
+    const long w0 = (long)unit * a.T;
+    off = (int)(w0 & 3);
+    w = a.weight + (w0 - off);
+    N = n;
+    const int nv = (N + off + 3) / 4, per_cta = (nv + ctas - 1) / ctas, per_warp = (per_cta + warps - 1) / warps;
+    v0 = rank * per_cta + (int)(threadIdx.x >> 5) * per_warp;
+    v1 = min(min(nv, (rank + 1) * per_cta), v0 + per_warp);
   }
-  const int N = L - a.recent, c = a.keep - a.recent;
-  for (int i = t; i < a.recent; i += step) kept[c + i] = N + i;
-  if (c == 0) return;
-  // 16-byte aligned vectors: vector v holds weights 4 v - off ..
-  const long w0 = (long)unit * a.T;
-  const int off = (int)(w0 & 3);
-  const float* w = a.weight + (w0 - off);
-  const int nv = (N + off + 3) / 4, per_cta = (nv + ctas - 1) / ctas, per_warp = (per_cta + 31) / 32;
-  const int end_cta = min(nv, (rank + 1) * per_cta), v0 = rank * per_cta + warp * per_warp;
-  const int v1 = min(end_cta, v0 + per_warp);
-  uint32_t key[kSelVec][4];
-  auto load = [&](int base) {  // keys of this lane's vectors; 0 where there is no weight
+  __device__ __forceinline__ bool whole(int v) const { return v < v1 && 4 * v - off >= 0 && 4 * v - off + 3 < N; }
+  __device__ __forceinline__ void fetch(int base) {
 #pragma unroll
-    for (int s = 0; s < kSelVec; ++s) {
-      const int v = base + s * 32 + lane, e = 4 * v - off;
-      if (v < v1 && e >= 0 && e + 3 < N) {
-        const float4 x = __ldg(reinterpret_cast<const float4*>(w) + v);
-        key[s][0] = weight_key(x.x);
-        key[s][1] = weight_key(x.y);
-        key[s][2] = weight_key(x.z);
-        key[s][3] = weight_key(x.w);
+    for (int s = 0; s < VEC; ++s) {
+      const int v = base + s * 32 + (int)(threadIdx.x & 31);
+      if (whole(v)) ahead[s] = __ldg(reinterpret_cast<const float4*>(w) + v);
+    }
+  }
+  __device__ __forceinline__ void keys(int base) {  // 0 where there is no weight
+#pragma unroll
+    for (int s = 0; s < VEC; ++s) {
+      const int v = base + s * 32 + (int)(threadIdx.x & 31), e = 4 * v - off;
+      if (whole(v)) {
+        key[s][0] = weight_key(ahead[s].x);
+        key[s][1] = weight_key(ahead[s].y);
+        key[s][2] = weight_key(ahead[s].z);
+        key[s][3] = weight_key(ahead[s].w);
       } else {
 #pragma unroll
         for (int x = 0; x < 4; ++x)
           key[s][x] = v < v1 && e + x >= 0 && e + x < N ? weight_key(__ldg(w + 4L * v + x)) : 0u;
       }
     }
-  };
-  if (REG) load(v0);
-  for (int i = tid; i < 3 * 2048; i += kSelThr) hist[0][i] = 0u;
-  __syncthreads();
-  uint32_t prefix = 0u, need = (uint32_t)c;
-#pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
+  }
+  __device__ __forceinline__ void count(uint32_t* hist, int pass, uint32_t prefix) const {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const uint32_t mask = pass == 0 ? 0u : pass == 1 ? 0xFFE00000u : 0xFFFFFC00u, digit = pass == 2 ? 1023u : 2047u;
-    for (int base = v0; base < v1; base += kSelWarp) {
-      if (!REG) load(base);
 #pragma unroll
-      for (int s = 0; s < kSelVec; ++s)
+    for (int s = 0; s < VEC; ++s)
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-          if (key[s][x] && (key[s][x] & mask) == prefix) atomicAdd(&hist[pass][(key[s][x] >> shift) & digit], 1u);
-      if (REG) break;
-    }
-    cluster.sync();
-    // bins from the top: the one that holds the need-th
-    uint32_t n0 = 0u, n1 = 0u;
-    for (int r = 0; r < ctas; ++r) {
-      const uint2 h = *cluster.map_shared_rank(reinterpret_cast<uint2*>(&hist[pass][2046 - 2 * tid]), r);
-      n0 += h.y;
-      n1 += h.x;
-    }
-    uint32_t all;
-    const uint32_t before = block_scan(n0 + n1, buf, &all);
-    if (before < need && need <= before + n0 + n1) {
-      const bool second = need > before + n0;
-      s_bin = 2047u - 2u * tid - (second ? 1u : 0u);
-      s_need = need - before - (second ? n0 : 0u);
-    }
-    __syncthreads();
-    prefix |= s_bin << shift;
-    need = s_need;
+      for (int x = 0; x < 4; ++x)
+        if (key[s][x] && (key[s][x] & mask) == prefix) atomicAdd(&hist[(key[s][x] >> shift) & digit], 1u);
   }
-  const uint32_t thr = prefix, ties = need;
-  // heavier ones and equals in this warp, this CTA's warps before it, the CTAs before this one
-  uint32_t gt = 0u, eq = 0u;
-  for (int base = v0; base < v1; base += kSelWarp) {
-    if (!REG) load(base);
+  __device__ __forceinline__ void above(uint32_t thr, uint32_t& gt, uint32_t& eq) const {
 #pragma unroll
-    for (int s = 0; s < kSelVec; ++s)
+    for (int s = 0; s < VEC; ++s)
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         gt += key[s][x] > thr ? 1u : 0u;
         eq += key[s][x] == thr ? 1u : 0u;
       }
-    if (REG) break;
   }
-  gt = __reduce_add_sync(0xFFFFFFFFu, gt);
-  eq = __reduce_add_sync(0xFFFFFFFFu, eq);
-  uint32_t all_gt, all_eq;
-  uint32_t ng = block_scan(lane == 0 ? gt : 0u, buf, &all_gt), ne = block_scan(lane == 0 ? eq : 0u, buf, &all_eq);
-  ng = __shfl_sync(0xFFFFFFFFu, ng, 0);
-  ne = __shfl_sync(0xFFFFFFFFu, ne, 0);
-  if (tid == 0) {
-    s_count[0] = all_gt;
-    s_count[1] = all_eq;
-  }
-  cluster.sync();
-  for (int r = 0; r < rank; ++r) {
-    const uint32_t* x = cluster.map_shared_rank(&s_count[0], r);
-    ng += x[0];
-    ne += x[1];
-  }
-  const uint32_t below = (1u << lane) - 1u;
-  for (int base = v0; base < v1; base += kSelWarp) {
-    if (!REG) load(base);
+  // ng heavier ones and ne equals precede these vectors; both go on behind them
+  __device__ __forceinline__ void emit(int base, uint32_t thr, uint32_t ties, uint32_t& ng, uint32_t& ne,
+                                       int32_t* kept) const {
+    const int lane = threadIdx.x & 31;
+    const uint32_t below = (1u << lane) - 1u;
 #pragma unroll
-    for (int s = 0; s < kSelVec; ++s) {
+    for (int s = 0; s < VEC; ++s) {
       uint32_t lg = 0u, le = 0u, ag = 0u, ae = 0u;  // in the lanes below, in all lanes
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
@@ -184,9 +128,179 @@ __global__ void __launch_bounds__(kSelThr) cache8_keep_kernel(C8EvictArgs a) {
       ng += ag;
       ne += ae;
     }
-    if (REG) break;
   }
+};
+
+// Thread t of 1024 holds the counts n0, n1 of bins 2047 - 2 t and 2046 - 2 t: extends the prefix by the
+// bin of the need-th heaviest, and counts need from the top of that bin.
+__device__ __forceinline__ void find_bin(uint32_t n0, uint32_t n1, int pass, uint32_t& prefix, uint32_t& need,
+                                         uint32_t* buf, uint32_t* found) {
+  uint32_t all;
+  const uint32_t before = block_scan(n0 + n1, buf, &all);
+  if (before < need && need <= before + n0 + n1) {
+    const bool second = need > before + n0;
+    found[0] = 2047u - 2u * threadIdx.x - (second ? 1u : 0u);
+    found[1] = need - before - (second ? n0 : 0u);
+  }
+  __syncthreads();
+  prefix |= found[0] << (pass == 0 ? 21 : pass == 1 ? 10 : 0);
+  need = found[1];
+}
+
+// What needs no selection: thread t of n writes its share. True if there is nothing more to do.
+__device__ __forceinline__ bool keep_simple(const C8EvictArgs& a, int unit, int L, int t, int n) {
+  const int m = min(L, a.keep), c = a.keep - a.recent;
+  int32_t* kept = a.kept + (long)unit * a.keep;
+  if (unit % a.G == 0 && t == 0) a.lens_out[unit / a.G] = m;
+  for (int i = m + t; i < a.keep; i += n) kept[i] = -1;
+  if (L <= a.keep) {
+    for (int i = t; i < L; i += n) kept[i] = i;
+    return true;
+  }
+  for (int i = t; i < a.recent; i += n) kept[c + i] = L - a.recent + i;
+  return c == 0;
+}
+
+// Of more than `keep` tokens the `recent` last stay, and of the N before them the c = keep - recent
+// heaviest: a radix select (11, 11 and 10 bits) finds the key of the c-th heaviest and how many of its
+// equals stay, the lowest positions first; an ordered pass writes the positions. A cluster of CTAs
+// serves one (sequence, group): each histograms its part of the weights (a contiguous range, split
+// into one per warp) in its own shared memory and adds up the others' over distributed shared memory.
+// REG: a part fits the CTA's registers, VEC 16-byte loads a lane, and is read once; else it is read in
+// every pass (from L2), the next loads under way while the present ones are counted.
+template <int VEC, bool REG>
+__global__ void __launch_bounds__(kSelThr) cache8_keep_kernel(C8EvictArgs a) {
+  __shared__ alignas(16) uint32_t hist[3][2048];
+  __shared__ uint32_t buf[32], found[2], s_count[2];
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
+  const int unit = blockIdx.x / ctas, tid = threadIdx.x, lane = tid & 31;
+  const int L = c8_len(a.lens, unit / a.G, a.T, a.status);
+  if (keep_simple(a, unit, L, rank * kSelThr + tid, ctas * kSelThr)) return;
+  Part<VEC> part;
+  part.set(a, unit, L - a.recent, ctas, rank, 32);
+  // a pass over the part: take(base) with the keys of vectors base ..
+  auto pass_over = [&](auto&& take) {
+    if (REG) {
+      take(part.v0);
+    } else {
+      part.fetch(part.v0);
+      for (int base = part.v0; base < part.v1; base += VEC * 32) {
+        part.keys(base);
+        if (base + VEC * 32 < part.v1) part.fetch(base + VEC * 32);
+        take(base);
+      }
+    }
+  };
+  if (REG) part.fetch(part.v0);
+  for (int i = tid; i < 3 * 2048; i += kSelThr) hist[0][i] = 0u;
+  if (REG) part.keys(part.v0);
+  __syncthreads();
+  uint32_t prefix = 0u, need = (uint32_t)(a.keep - a.recent);
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    pass_over([&](int) { part.count(hist[pass], pass, prefix); });
+    cluster.sync();
+    uint32_t n0 = 0u, n1 = 0u;
+    for (int r = 0; r < ctas; ++r) {
+      const uint2 h = *cluster.map_shared_rank(reinterpret_cast<uint2*>(&hist[pass][2046 - 2 * tid]), r);
+      n0 += h.y;
+      n1 += h.x;
+    }
+    find_bin(n0, n1, pass, prefix, need, buf, found);
+  }
+  // heavier ones and equals in this warp, this CTA's warps before it, the CTAs before this one
+  uint32_t gt = 0u, eq = 0u;
+  pass_over([&](int) { part.above(prefix, gt, eq); });
+  gt = __reduce_add_sync(0xFFFFFFFFu, gt);
+  eq = __reduce_add_sync(0xFFFFFFFFu, eq);
+  uint32_t all_gt, all_eq;
+  uint32_t ng = block_scan(lane == 0 ? gt : 0u, buf, &all_gt), ne = block_scan(lane == 0 ? eq : 0u, buf, &all_eq);
+  ng = __shfl_sync(0xFFFFFFFFu, ng, 0);
+  ne = __shfl_sync(0xFFFFFFFFu, ne, 0);
+  if (tid == 0) {
+    s_count[0] = all_gt;
+    s_count[1] = all_eq;
+  }
+  cluster.sync();
+  for (int r = 0; r < rank; ++r) {
+    const uint32_t* x = cluster.map_shared_rank(&s_count[0], r);
+    ng += x[0];
+    ne += x[1];
+  }
+  int32_t* kept = a.kept + (long)unit * a.keep;
+  pass_over([&](int base) { part.emit(base, prefix, need, ng, ne, kept); });
   cluster.sync();  // no CTA leaves while another reads its shared memory
+}
+
+// The same selection for few (sequence, group)s of very many weights, which need the whole GPU: a part
+// of 16384 weights per CTA, and a launch per pass (STEP 0 to 2: histograms, added up in global memory;
+// 3: counts of every part; 4: positions). The weights come from L2 after the first.
+// Global memory, per unit: 3 histograms, (prefix, need) after each, (heavier, equal) of every part.
+template <int STEP>
+__global__ void __launch_bounds__(kSelThr) cache8_keep_grid_kernel(C8EvictArgs a) {
+  __shared__ alignas(16) uint32_t hist[STEP < 3 ? 2048 : 2];
+  __shared__ uint32_t buf[32], found[2];
+  const int unit = blockIdx.y, rank = blockIdx.x, ctas = gridDim.x, tid = threadIdx.x, lane = tid & 31;
+  const int L = c8_len(a.lens, unit / a.G, a.T, a.status);
+  if (STEP == 0) {
+    if (keep_simple(a, unit, L, rank * kSelThr + tid, ctas * kSelThr)) return;
+  } else if (L <= a.keep || a.keep == a.recent) {
+    return;
+  }
+  uint32_t* g = a.grid_ws + (long)unit * keep_grid_words(ctas);
+  uint32_t* state = g + 3 * 2048;  // [3][2]
+  uint2* counts = reinterpret_cast<uint2*>(state + 8);
+  Part<4> part;
+  part.set(a, unit, L - a.recent, ctas, rank, 32);
+  part.fetch(part.v0);
+  uint32_t prefix = 0u, need = (uint32_t)(a.keep - a.recent);
+  if (STEP < 3)
+    for (int i = tid; i < 2048; i += kSelThr) hist[i] = 0u;
+  if (STEP > 1) {
+    prefix = state[2 * (min(STEP, 4) - 2)];
+    need = state[2 * (min(STEP, 4) - 2) + 1];
+  }
+  if (STEP > 0 && STEP < 4) {
+    const uint2 h = *reinterpret_cast<const uint2*>(g + (STEP - 1) * 2048 + 2046 - 2 * tid);
+    find_bin(h.y, h.x, STEP - 1, prefix, need, buf, found);
+    if (rank == 0 && tid == 0) {
+      state[2 * (STEP - 1)] = prefix;
+      state[2 * (STEP - 1) + 1] = need;
+    }
+  } else {
+    __syncthreads();
+  }
+  part.keys(part.v0);
+  if constexpr (STEP < 3) {
+    part.count(hist, STEP, prefix);
+    __syncthreads();
+    for (int i = tid; i < 2048; i += kSelThr)
+      if (hist[i]) atomicAdd(g + STEP * 2048 + i, hist[i]);
+  } else {
+    uint32_t gt = 0u, eq = 0u, all_gt, all_eq;
+    part.above(prefix, gt, eq);
+    gt = __reduce_add_sync(0xFFFFFFFFu, gt);
+    eq = __reduce_add_sync(0xFFFFFFFFu, eq);
+    uint32_t ng = block_scan(lane == 0 ? gt : 0u, buf, &all_gt), ne = block_scan(lane == 0 ? eq : 0u, buf, &all_eq);
+    if constexpr (STEP == 3) {
+      if (tid == 0) counts[rank] = make_uint2(all_gt, all_eq);
+    } else {
+      ng = __shfl_sync(0xFFFFFFFFu, ng, 0);
+      ne = __shfl_sync(0xFFFFFFFFu, ne, 0);
+      uint32_t bg = 0u, be = 0u, before_g, before_e;
+      for (int r = tid; r < rank; r += kSelThr) {
+        const uint2 x = counts[r];
+        bg += x.x;
+        be += x.y;
+      }
+      block_scan(bg, buf, &before_g);
+      block_scan(be, buf, &before_e);
+      ng += before_g;
+      ne += before_e;
+      part.emit(part.v0, prefix, need, ng, ne, a.kept + (long)unit * a.keep);
+    }
+  }
 }
 
 constexpr int kThr = 256;
@@ -207,12 +321,6 @@ __device__ __forceinline__ uint32_t amax16(const uint4& x, float scale) {
   }
   return __float_as_uint(c8_decode2(m).x * scale);
 }
-__device__ __forceinline__ uint4 rescale16(const uint4& x, int k) {
-  if (k == 0) return x;
-  const float f = c8_shift(k);
-  return make_uint4(c8_rescale4(x.x, f), c8_rescale4(x.y, f), c8_rescale4(x.z, f), c8_rescale4(x.w, f));
-}
-
 // One item per block of the new cache and group, rows and items as in the append kernel. HBM bound: a
 // kept row is read and written once.
 constexpr int kLoop = 8;
@@ -232,38 +340,60 @@ __global__ void __launch_bounds__(kThr) cache8_move_kernel(C8EvictArgs a, int lo
   const int row0 = kItems > 1 ? (tid / kTpr) % BLK : tid / kTpr;
   const int col = (tid % kTpr) * 16;
   const int nblk = (a.T + BLK - 1) / BLK, nblk_out = (a.T_out + BLK - 1) / BLK;
-  int j = (first + sub) / a.G, g = (first + sub) % a.G;
-  for (int it = 0; it < loop; ++it) {
+  // One step ahead: the rows' positions; with one or two rows per thread also the rows themselves.
+  constexpr bool kAhead = kPass == 2;
+  struct Item {
+    int j, g, u[kPass];
     uint4 xk[kPass], xv[kPass];
-    int ek[kPass], ev[kPass], u[kPass];
-    uint32_t mk = 0, mv = 0;
-    const int i0 = j * BLK + row0;
-#pragma unroll
-    for (int p = 0; p < kPass; ++p)
-      u[p] = i0 + p * kRows < m ? __ldg(a.kept + (long)(b * a.G + g) * a.keep + i0 + p * kRows) : -1;
+    int ek[kPass], ev[kPass];
+  };
+  auto positions = [&](Item& x) {
 #pragma unroll
     for (int p = 0; p < kPass; ++p) {
-      xk[p] = xv[p] = make_uint4(0, 0, 0, 0);
-      ek[p] = ev[p] = -126;
-      if (u[p] >= 0) {
-        const long src = (long)((b * a.T + u[p]) * a.G + g) * D + col;
-        const long si = (long)(b * nblk + u[p] / BLK) * a.G + g;
-        xk[p] = __ldg(reinterpret_cast<const uint4*>(a.src.k8 + src));
-        xv[p] = __ldg(reinterpret_cast<const uint4*>(a.src.v8 + src));
-        ek[p] = c8_scale_exponent(__ldg(a.src.ks + si));
-        ev[p] = c8_scale_exponent(__ldg(a.src.vs + si));
+      const int i = x.j * BLK + row0 + p * kRows;
+      x.u[p] = i < m ? __ldg(a.kept + (long)(b * a.G + x.g) * a.keep + i) : -1;
+    }
+  };
+  auto fetch = [&](Item& x) {
+#pragma unroll
+    for (int p = 0; p < kPass; ++p) {
+      x.xk[p] = x.xv[p] = make_uint4(0, 0, 0, 0);
+      x.ek[p] = x.ev[p] = -126;
+      if (x.u[p] >= 0) {
+        const long src = (long)((b * a.T + x.u[p]) * a.G + x.g) * D + col;
+        const long si = (long)(b * nblk + x.u[p] / BLK) * a.G + x.g;
+        x.xk[p] = __ldg(reinterpret_cast<const uint4*>(a.src.k8 + src));
+        x.xv[p] = __ldg(reinterpret_cast<const uint4*>(a.src.v8 + src));
+        x.ek[p] = c8_scale_exponent(__ldg(a.src.ks + si));
+        x.ev[p] = c8_scale_exponent(__ldg(a.src.vs + si));
       }
     }
+  };
+  auto next = [&](Item& y, const Item& x) {
+    y.j = x.j;
+    for (y.g = x.g + kItems; y.g >= a.G; y.g -= a.G) ++y.j;
+  };
+  Item x, y;
+  x.j = (first + sub) / a.G;
+  x.g = (first + sub) % a.G;
+  positions(x);
+  if (kAhead) fetch(x);
+  for (int it = 0; it < loop; ++it) {
+    next(y, x);
+    if (it + 1 < loop) positions(y);
+    if (!kAhead) fetch(x);
+    const int i0 = x.j * BLK + row0;
     if (col == 0) {
 #pragma unroll
       for (int p = 0; p < kPass; ++p)
-        if (u[p] >= 0)
-          a.w_out[(long)(b * a.G + g) * a.T_out + i0 + p * kRows] = __ldg(a.weight + (long)(b * a.G + g) * a.T + u[p]);
+        if (x.u[p] >= 0)
+          a.w_out[(long)(b * a.G + x.g) * a.T_out + i0 + p * kRows] = __ldg(a.weight + (long)(b * a.G + x.g) * a.T + x.u[p]);
     }
+    uint32_t mk = 0, mv = 0;
 #pragma unroll
     for (int p = 0; p < kPass; ++p) {
-      mk = max(mk, amax16(xk[p], c8_pow2(ek[p])));
-      mv = max(mv, amax16(xv[p], c8_pow2(ev[p])));
+      mk = max(mk, amax16(x.xk[p], c8_pow2(x.ek[p])));
+      mv = max(mv, amax16(x.xv[p], c8_pow2(x.ev[p])));
     }
     mk = __reduce_max_sync(0xFFFFFFFFu, mk);
     mv = __reduce_max_sync(0xFFFFFFFFu, mv);
@@ -271,21 +401,22 @@ __global__ void __launch_bounds__(kThr) cache8_move_kernel(C8EvictArgs a, int lo
       atomicMax(&amax[it][sub][0], mk);
       atomicMax(&amax[it][sub][1], mv);
     }
+    if (kAhead && it + 1 < loop) fetch(y);
     __syncthreads();
     const int nk = c8_exponent(amax[it][sub][0]), nv = c8_exponent(amax[it][sub][1]);
 #pragma unroll
     for (int p = 0; p < kPass; ++p) {
-      if (u[p] < 0) break;
-      const long dst = (long)((b * a.T_out + i0 + p * kRows) * a.G + g) * D + col;
-      *reinterpret_cast<uint4*>(a.dst.k8 + dst) = rescale16(xk[p], ek[p] - nk);
-      *reinterpret_cast<uint4*>(a.dst.v8 + dst) = rescale16(xv[p], ev[p] - nv);
+      if (x.u[p] < 0) break;
+      const long dst = (long)((b * a.T_out + i0 + p * kRows) * a.G + x.g) * D + col;
+      *reinterpret_cast<uint4*>(a.dst.k8 + dst) = c8_rescale16(x.xk[p], x.ek[p] - nk);
+      *reinterpret_cast<uint4*>(a.dst.v8 + dst) = c8_rescale16(x.xv[p], x.ev[p] - nv);
     }
-    if (row0 == 0 && col == 0 && u[0] >= 0) {
-      const long so = (long)(b * nblk_out + j) * a.G + g;
+    if (row0 == 0 && col == 0 && x.u[0] >= 0) {
+      const long so = (long)(b * nblk_out + x.j) * a.G + x.g;
       a.dst.ks[so] = c8_pow2(nk);
       a.dst.vs[so] = c8_pow2(nv);
     }
-    for (g += kItems; g >= a.G; g -= a.G) ++j;
+    x = y;
   }
 }
 
@@ -313,15 +444,10 @@ cudaError_t launch_d(const C8EvictArgs& a, cudaStream_t s) {
 }
 
 // A part that starts and ends inside a vector still fits the registers of ctas CTAs.
-bool keep_fits(int T, int ctas) { return (long)T + 6 <= (long)kSelCta * ctas; }
-// CTAs per (sequence, group): as few as hold its weights in registers, up to a cluster's 8, and more
-// while that leaves SMs without a CTA and a part 2048 weights or more.
-int keep_ctas(long units, int T) {
-  int c = 1;
-  while (c < 8 && (!keep_fits(T, c) || (units * c * 2 <= 148 && T >= c * 2 * 2048))) c *= 2;
-  return c;
-}
-template <bool REG>
+bool keep_fits(int T, int vec, int ctas) { return (long)T + (T % 4 ? 6 : 0) <= (long)kSelPart * vec * ctas; }
+
+// Clusters of 16 where the device can hold one (8 are always possible).
+template <int VEC, bool REG>
 cudaError_t launch_keep(const C8EvictArgs& a, int ctas, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at{};
@@ -333,14 +459,59 @@ cudaError_t launch_keep(const C8EvictArgs& a, int ctas, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache8_keep_kernel<REG>, a);
+  if (ctas == 16) {
+    static const bool can = [&] {
+      int n = 0;
+      const bool ok = cudaFuncSetAttribute(cache8_keep_kernel<VEC, REG>, cudaFuncAttributeNonPortableClusterSizeAllowed,
+                                           1) == cudaSuccess &&
+                      cudaOccupancyMaxActiveClusters(&n, cache8_keep_kernel<VEC, REG>, &cfg) == cudaSuccess && n > 0;
+      if (!ok) (void)cudaGetLastError();
+      return ok;
+    }();
+    if (!can) {
+      at.val.clusterDim.x = 8;
+      cfg.gridDim = dim3((unsigned)(a.batch * a.G * 8));
+    }
+  }
+  return cudaLaunchKernelEx(&cfg, cache8_keep_kernel<VEC, REG>, a);
+}
+// Which selection: clusters of as few CTAs as hold a (sequence, group)'s weights in registers with four
+// loads a lane, up to 8; of more while that leaves SMs without a CTA and a part 2048 weights or more.
+// Where 8 do not hold them: launches over the whole GPU if clusters of 16 would leave SMs without a CTA
+// (1M weights, 4 groups: 76 us with 4 clusters of 16), else those.
+bool keep_on_grid(long units, int T) { return !keep_fits(T, 4, 8) && units * 16 <= 148; }
+int keep_grid_ctas(int T) { return (int)(((long)T + 6 + 4 * kSelPart - 1) / (4 * kSelPart)); }
+cudaError_t launch_keep_any(const C8EvictArgs& a, cudaStream_t s) {
+  const long units = (long)a.batch * a.G;
+  if (keep_on_grid(units, a.T)) {
+    const int ctas = keep_grid_ctas(a.T);
+    cudaError_t e = cudaMemsetAsync(a.grid_ws, 0, (size_t)units * keep_grid_words(ctas) * 4, s);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)ctas, (unsigned)units);
+    cache8_keep_grid_kernel<0><<<grid, kSelThr, 0, s>>>(a);
+    cache8_keep_grid_kernel<1><<<grid, kSelThr, 0, s>>>(a);
+    cache8_keep_grid_kernel<2><<<grid, kSelThr, 0, s>>>(a);
+    cache8_keep_grid_kernel<3><<<grid, kSelThr, 0, s>>>(a);
+    cache8_keep_grid_kernel<4><<<grid, kSelThr, 0, s>>>(a);
+    return cudaGetLastError();
+  }
+  int c = 1;
+  while (c < 8 && (!keep_fits(a.T, 4, c) || (units * c * 2 <= 148 && a.T >= c * 2 * 2048))) c *= 2;
+  if (keep_fits(a.T, 1, c)) return launch_keep<1, true>(a, c, s);
+  if (keep_fits(a.T, 2, c)) return launch_keep<2, true>(a, c, s);
+  if (keep_fits(a.T, 4, c)) return launch_keep<4, true>(a, c, s);
+  return launch_keep<4, false>(a, 16, s);
 }
 
 }  // namespace
 
+size_t cache8_keep_bytes(int batch, int G, int T) {
+  const long units = (long)batch * G;
+  return keep_on_grid(units, T) ? (size_t)units * keep_grid_words(keep_grid_ctas(T)) * 4 : 0;
+}
+
 cudaError_t launch_cache8_evict(const C8EvictArgs& a, cudaStream_t s) {
-  const int ctas = keep_ctas((long)a.batch * a.G, a.T);
-  const cudaError_t e = keep_fits(a.T, ctas) ? launch_keep<true>(a, ctas, s) : launch_keep<false>(a, ctas, s);
+  const cudaError_t e = launch_keep_any(a, s);
   if (e != cudaSuccess) return e;
   return a.d == 64 ? launch_d<64>(a, s) : launch_d<128>(a, s);
 }
