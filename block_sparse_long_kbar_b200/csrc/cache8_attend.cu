@@ -37,7 +37,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNegMax = -3.4028234663852886e38f;  // maximum of a row that no token has reached
 constexpr int kTok = 128;                           // tokens per tile
 constexpr int kGridMax = 148;                       // one CTA per SM
-constexpr int kThreads = 512;
 constexpr int kMaxNR = 32;                          // rows per unit; more make several units
 constexpr int kNever = 0x7FFFFFFF;
 
@@ -46,32 +45,41 @@ struct Cfg {
   static constexpr int N = 2 * NR;                       // MMA columns: both terms of every row
   static constexpr int kTile = kTok * D;
   static constexpr int kStage = W ? kTile : 2 * kTile;   // K, then V
-  static constexpr int kStages = D == 128 ? (W ? 8 : 5) : (W ? 8 : 8);
+  static constexpr int kStages = D == 64 || W ? 8 : 5;
   static constexpr int kQ = N * D;
   static constexpr int kP = W ? 0 : kTok * N;
-  static constexpr int kTmem = (W ? 2 : 4) * N < 32 ? 32 : (W ? 2 : 4) * N;
+  // Softmax groups of four warps, each with a buffer of S^T, P and O^T of its own. Two keep up with
+  // HBM where a tile is 32 KB and has up to 16 rows; 32 rows took 1350 cycles a tile with two.
+  static constexpr int kGroups = W || D == 64 || NR == 32 ? 3 : 2;
+  static constexpr int kThreads = 128 + 128 * kGroups + (W ? 0 : 128);
+  static constexpr int kTmemUsed = (W ? 1 : 2) * kGroups * N;
+  static constexpr int kTmem = kTmemUsed <= 64 ? 64 : kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
+  static constexpr int kQWarps = W ? 2 : 4;              // warps that split q
   static constexpr int kRowsT = D == 128 ? NR : NR / 2;  // rows per accumulating thread
   static constexpr int q = NR / 4;                       // rows per lane of the softmax warps
 };
 
+constexpr int kMaxGroups = 3;
 template <int NR>
 struct Shared {
   uint64_t full[8], empty[8];
-  float scale[8][32];       // per stage: K scales of the tile's blocks, then V scales
-  uint64_t s_full[2], s_empty[2], p_full[2], o_full[2], o_empty[2], q_full[2], q_empty[2];
+  uint64_t s_full[kMaxGroups], s_empty[kMaxGroups], p_full[kMaxGroups], o_full[kMaxGroups], o_empty[kMaxGroups];
+  uint64_t f_full[kMaxGroups], q_full[2], q_empty[2];
+  float scale[8][32];                      // per stage: K scales of the tile's blocks, then V scales
   uint32_t tmem;
   volatile int abort_flag;
-  int start_b, start_off, total;
-  int wsum[kThreads / 32];
+  int start_b, start_off;
+  int wsum[32];
   int nan_any[2];
-  int nan_at[2][128];       // per head dim: first token not visible to all rows whose V is NaN there
-  int wev[2][4];
-  alignas(16) float fac[2][NR];  // per unit parity: 2^e log2 e / sqrt(d) of a row
+  int nan_at[2][128];                      // per head dim: first token not visible to all rows whose V is NaN there
+  int wev[kMaxGroups][4];
+  alignas(16) float fac[2][NR];            // per unit parity: 2^e log2 e / sqrt(d) of a row
   float lse[2][NR];
-  int lim[2][NR];           // a row's own position; -1: no row
-  alignas(16) float wmax[2][4][NR];  // per softmax group and warp: a row's maximum over the tile
-  alignas(16) float wsum_p[2][4][NR];  // and the sum of its probabilities
-  alignas(16) float acc_a[2][NR], acc_b[2][NR];  // factors of the sums so far and of this tile
+  int lim[2][NR];                          // a row's own position; -1: no row
+  alignas(16) float wmax[kMaxGroups][4][NR];    // per softmax group and warp: a row's maximum over the tile
+  alignas(16) float wsum_p[kMaxGroups][4][NR];  // and the sum of its probabilities
+  // per softmax group: factors of the sums so far (x, y) and of this tile (z, w) for pairs of rows
+  float4 acc[kMaxGroups][NR / 2];
 };
 
 // The tiles of one CTA in order, a piece of a unit at a time: tiles [t0, t1) of unit ((sequence b,
@@ -190,6 +198,12 @@ __device__ __forceinline__ void tmem_ld_frag<8>(uint32_t taddr, uint32_t (&c)[64
       : "memory");
 }
 
+// the largest; NaN only if all are
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
 // pairs of fp32
 __device__ __forceinline__ uint64_t pack2(float x, float y) {
   uint64_t r;
@@ -300,7 +314,7 @@ __device__ __forceinline__ void split_q(const C8AttendArgs& a, const Walk& w, Sh
 #pragma unroll
     for (int y = 0; y < 8; ++y) {
       const int r = r8 + y * r_step;
-      if (r >= NR) break;
+      if (r < NR) {
       uint32_t amax = 0u;
 #pragma unroll
       for (int e = 0; e < kE / 2; ++e) {
@@ -336,16 +350,33 @@ __device__ __forceinline__ void split_q(const C8AttendArgs& a, const Walk& w, Sh
         *reinterpret_cast<uint16_t*>(p2) = (uint16_t)c2;
       }
       if (lane == 0) sh.fac[pb][r] = c8_pow2(ex) * (kLog2e / sqrtf((float)D));
+      }
     }
   }
   tc::fence_proxy_async();
 }
 
+// One of the warps that split q: rows first, first + kQWarps, .. of the piece w, and of all pieces.
 template <int D, int NR, bool W>
-__global__ void __launch_bounds__(kThreads, 1)
+__device__ __forceinline__ void split_piece(const C8AttendArgs& a, const Walk& w, Shared<NR>& sh, uint8_t* sQ, int first,
+                                            volatile int* abort, int lane) {
+  const int pb = w.piece & 1;
+  if (w.piece >= 2) warp_wait(&sh.q_empty[pb], (uint32_t)(((w.piece >> 1) - 1) & 1), abort, a.status);
+  split_q<D, NR, W>(a, w, sh, sQ, first, Cfg<D, NR, W>::kQWarps, lane);
+  tc::mbar_arrive(&sh.q_full[pb]);
+}
+template <int D, int NR, bool W>
+__device__ __forceinline__ void split_all(const C8AttendArgs& a, Walk w, Shared<NR>& sh, uint8_t* sQ, int first,
+                                          volatile int* abort, int lane) {
+  for (; w.left > 0; walk_next(w, a)) split_piece<D, NR, W>(a, w, sh, sQ, first, abort, lane);
+}
+
+template <int D, int NR, bool W>
+__global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
     cache8_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                          const C8AttendArgs a) {
   using C = Cfg<D, NR, W>;
+  constexpr int kThreads = C::kThreads, kGroups = C::kGroups;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared<NR> sh;
   uint8_t* sKV = smem_align<1024>(smem_raw);
@@ -364,14 +395,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(&sh.full[i], 1 + 32);
       tc::mbar_init(&sh.empty[i], W ? 1 + 4 : 1);  // the weights' pass reads scales after the MMA
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kGroups; ++i) {
       tc::mbar_init(&sh.s_full[i], 1);
       tc::mbar_init(&sh.s_empty[i], 4);
       tc::mbar_init(&sh.p_full[i], 128);
+      tc::mbar_init(&sh.f_full[i], 32);
       tc::mbar_init(&sh.o_full[i], 1);
       tc::mbar_init(&sh.o_empty[i], 4);
-      tc::mbar_init(&sh.q_full[i], 32);
-      tc::mbar_init(&sh.q_empty[i], 1 + 8);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&sh.q_full[i], 32 * C::kQWarps);
+      tc::mbar_init(&sh.q_empty[i], 1 + 4 * kGroups);
       sh.nan_any[i] = 0;
     }
     sh.abort_flag = 0;
@@ -419,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = sh.tmem;
-  const uint32_t tmem_o = tmem + 2 * C::N;
+  const uint32_t tmem_o = tmem + kGroups * C::N;
   volatile int* abort = &sh.abort_flag;
   Walk w;
   walk_begin(w, a, sh.start_b, sh.start_off, t1 - t0);
@@ -468,17 +502,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t id_s = idesc_f8(C::N, false, false);
       const uint64_t dk = tc::smem_desc_kmajor(sKV, D), dq = tc::smem_desc_kmajor_noswz(sQ, 128, D * 8);
       volatile int none = 0;
-      int k = 0, st = 0;
-      uint32_t ph = 0, sph = 0;  // phases of the stages and of S^T's buffers
+      int k = 0, st = 0, sb = 0;
+      uint32_t ph = 0, sph = 1;  // phases of the stages and of S^T's buffers
       bool ok = true;
       for (; w.left > 0 && ok; walk_next(w, a)) {
         const int pb = w.piece & 1;
         const uint64_t db = dq + (uint32_t)(pb * (C::kQ >> 4));
         ok = tc::mbar_wait(&sh.q_full[pb], (uint32_t)((w.piece >> 1) & 1), abort, a.status);
         for (int n = w.t1 - w.t0; n > 0 && ok; --n, ++k) {
-          const int sb = k & 1;
           if (!tc::mbar_wait(&sh.full[st], ph, abort, a.status) ||
-              (k >= 2 && !tc::mbar_wait(&sh.s_empty[sb], sph ^ 1u, abort, a.status))) {
+              (k >= kGroups && !tc::mbar_wait(&sh.s_empty[sb], sph, abort, a.status))) {
             ok = false;
             break;
           }
@@ -490,7 +523,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::mma_commit(&sh.s_full[sb]);
           if (W) tc::mma_commit(&sh.empty[st]);
           if (n == 1) tc::mma_commit(&sh.q_empty[pb]);
-          sph ^= (uint32_t)sb;
+          if (++sb == kGroups) {
+            sb = 0;
+            sph ^= 1u;
+          }
           if (++st == C::kStages) {
             st = 0;
             ph ^= 1;
@@ -502,15 +538,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         *abort = 1;
       }
       // the MMAs in flight end before the CTA leaves
-      if (k > 0) tc::mbar_wait(&sh.s_full[(k - 1) & 1], (uint32_t)(((k - 1) >> 1) & 1), &none);
+      if (k > 0) tc::mbar_wait(&sh.s_full[(k - 1) % kGroups], (uint32_t)(((k - 1) / kGroups) & 1), &none);
       if (W && ok)
         for (int j = max(0, k - C::kStages); j < k; ++j)
           tc::mbar_wait(&sh.empty[j % C::kStages], (uint32_t)((j / C::kStages) & 1), abort);
       if (ok) tc::mbar_wait(&sh.q_empty[(w.piece - 1) & 1], (uint32_t)(((w.piece - 1) >> 1) & 1), abort);
     }
   } else if (warp == 2) {
-    // ---- MMAs of O^T ----
-    if (!W && lane == 0) {
+    // ---- MMAs of O^T (no such in the weights' pass, where this warp splits q too) ----
+    if constexpr (W) {
+      split_all<D, NR, W>(a, w, sh, sQ, 1, abort, lane);
+    } else if (lane == 0) {
       constexpr uint32_t id_o = idesc_f8(C::N, true, true);
       const uint64_t dv = D == 128 ? tc::smem_desc_mnmajor_sw128(sKV + C::kTile, 1024, 1024)
                                    : smem_desc_mnmajor_sw64_twice(sKV + C::kTile);
@@ -518,11 +556,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dp = tc::smem_desc_kmajor_noswz(sP, 128, 2048);
       volatile int none = 0;
       const int count = w.left;
-      int k = 0, st = 0;
+      int k = 0, st = 0, pb = 0;
+      uint32_t ph = 0;
       for (; k < count; ++k) {
-        const int pb = k & 1;
-        if (!tc::mbar_wait(&sh.p_full[pb], (uint32_t)((k >> 1) & 1), abort, a.status) ||
-            (k >= 2 && !tc::mbar_wait(&sh.o_empty[pb], (uint32_t)(((k >> 1) - 1) & 1), abort, a.status))) {
+        if (!tc::mbar_wait(&sh.p_full[pb], ph, abort, a.status) ||
+            (k >= kGroups && !tc::mbar_wait(&sh.o_empty[pb], ph ^ 1u, abort, a.status))) {
           if (!*abort) report(a.status, SGQA_ERR_TIMEOUT);
           *abort = 1;
           break;
@@ -535,25 +573,57 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::mma_commit(&sh.empty[st]);
         tc::mma_commit(&sh.o_full[pb]);
         if (++st == C::kStages) st = 0;
+        if (++pb == kGroups) {
+          pb = 0;
+          ph ^= 1u;
+        }
       }
-      if (k > 0) tc::mbar_wait(&sh.o_full[(k - 1) & 1], (uint32_t)(((k - 1) >> 1) & 1), &none);
+      if (k > 0) tc::mbar_wait(&sh.o_full[(k - 1) % kGroups], (uint32_t)(((k - 1) / kGroups) & 1), &none);
       for (int j = max(0, k - C::kStages); j < k; ++j)
         tc::mbar_wait(&sh.empty[j % C::kStages], (uint32_t)((j / C::kStages) & 1), &none);
     }
   } else if (warp == 3) {
-    // ---- rows of q (the first piece's with the accumulating warps) ----
-    for (; w.left > 0; walk_next(w, a)) {
-      const int pb = w.piece & 1;
-      if (w.piece >= 2) warp_wait(&sh.q_empty[pb], (uint32_t)(((w.piece >> 1) - 1) & 1), abort, a.status);
-      if (w.piece == 0) {
-        split_q<D, NR, W>(a, w, sh, sQ, 0, 5, lane);
-        asm volatile("bar.sync 4, 160;" ::: "memory");
-      } else {
-        split_q<D, NR, W>(a, w, sh, sQ, 0, 1, lane);
+    if constexpr (W) {
+      split_all<D, NR, W>(a, w, sh, sQ, 0, abort, lane);
+    } else {
+      // ---- a lane per row: running maxima, denominators, factors for the accumulating warps ----
+      float m_run = kNegMax, l = 0.f;
+      int e_run = -126, sb = 0;
+      uint32_t ph = 0;
+      for (; w.left > 0; walk_next(w, a)) {
+        for (int n = w.t1 - w.t0; n > 0; --n) {
+          warp_wait(&sh.p_full[sb], ph, abort, a.status);
+          const int et = max(max(sh.wev[sb][0], sh.wev[sb][1]), max(sh.wev[sb][2], sh.wev[sb][3])), en = max(e_run, et);
+          if (lane < NR) {
+            const float(&wm)[4][NR] = sh.wmax[sb];
+            const float(&ws)[4][NR] = sh.wsum_p[sb];
+            const float mt = fmaxf(fmaxf(wm[0][lane], wm[1][lane]), fmaxf(wm[2][lane], wm[3][lane]));
+            const float mn = fmaxf(m_run, mt), fa = ex2_approx(m_run - mn), fb = ex2_approx(mt - mn);
+            float* f = reinterpret_cast<float*>(&sh.acc[sb][lane >> 1]) + (lane & 1);
+            f[0] = fa * c8_pow2(max(-126, e_run - en));
+            f[2] = fb * c8_pow2(max(-126, et - en)) * (1.f / 448.f);
+            l = fmaf(l, fa, ((ws[0][lane] + ws[1][lane]) + (ws[2][lane] + ws[3][lane])) * fb);
+            m_run = mn;
+          }
+          e_run = en;
+          tc::mbar_arrive(&sh.f_full[sb]);
+          if (++sb == kGroups) {
+            sb = 0;
+            ph ^= 1u;
+          }
+        }
+        const long slot = (long)w.b * units_b + w.g * a.nch + w.ch + blockIdx.x;
+        if (lane < NR) {
+          part.m(slot)[lane] = m_run;
+          part.l(slot)[lane] = l;
+        }
+        if (lane == 0) *part.e(slot) = e_run;
+        m_run = kNegMax;
+        l = 0.f;
+        e_run = -126;
       }
-      tc::mbar_arrive(&sh.q_full[pb]);
     }
-  } else if (warp < 12) {
+  } else if (warp < 4 + 4 * kGroups) {
     // ---- scores, probabilities: lane = rows (lane % 4) q .. + q - 1 of tokens lane / 4 + 8 e ----
     constexpr int q = C::q;
     const int wg = (warp >> 2) - 1, q4 = warp & 3, t = tid & 127;
@@ -562,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t fac[q / 2];
 #pragma unroll
     for (int j = 0; j < q / 2; ++j) fac[j] = 0ull;
-    // tiles k = wg, wg + 2, ..: stage k mod the stages, phase of the buffers k / 2
+    // tiles k = wg, wg + groups, ..: stage k mod the stages, phase of the buffers kp = k / groups
     int st = wg;
     uint32_t ph = 0, kp = 0;
     for (; w.left > 0; walk_next(w, a)) {
@@ -572,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < q / 2; ++j) fac[j] = pack2(sh.fac[pb][row0 + 2 * j], sh.fac[pb][row0 + 2 * j + 1]);
       const int vis = w.L - a.n_new;  // tokens up to here are visible to every row
       const long wi0 = ((long)w.b * a.G + w.g) * a.T;
-      for (int tile = w.t0 + ((w.k ^ wg) & 1); tile < w.t1; tile += 2, ++kp) {
+      for (int tile = w.t0 + (wg + kGroups - w.k % kGroups) % kGroups; tile < w.t1; tile += kGroups, ++kp) {
         const int u0 = tile * kTok + tok;
         const bool edge = (tile + 1) * kTok - 1 > vis;
         const int uw = tile * kTok + q4 * 32 + (lane >> 2) + 8 * i;  // the token whose weight this lane writes
@@ -662,15 +732,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           float mx[q];
 #pragma unroll
           for (int j = 0; j < q / 2; ++j) {
-            float2 x = make_float2(kNegMax, kNegMax);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 y = unpack2(z[e][j]);
-              x.x = fmaxf(x.x, y.x);
-              x.y = fmaxf(x.y, y.y);
-            }
-            mx[2 * j] = x.x;
-            mx[2 * j + 1] = x.y;
+            const float2 z0 = unpack2(z[0][j]), z1 = unpack2(z[1][j]), z2 = unpack2(z[2][j]), z3 = unpack2(z[3][j]);
+            mx[2 * j] = max3(max3(z0.x, z1.x, z2.x), z3.x, kNegMax);
+            mx[2 * j + 1] = max3(max3(z0.y, z1.y, z2.y), z3.y, kNegMax);
           }
           const float mine = across_tokens<q>(mx, lane, [](float x, float y) { return fmaxf(x, y); });
           we = __reduce_max_sync(0xFFFFFFFFu, we);
@@ -682,20 +746,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             // A zero probability must not meet a NaN code: rows behind the last token become zeros,
             // and a NaN of a token that some row does not see is noted and taken out; the rows that
             // see it get it back at the end.
-            const int u = tile * kTok + t;
-            uint8_t* v = sKV + st * C::kStage + C::kTile + t * D;
-            if (u >= w.L) {
+            uint8_t* v = sKV + st * C::kStage + C::kTile;
+            const int after = w.L - tile * kTok;  // the tile's first row behind the last token
+            if (t >= after) {
 #pragma unroll
-              for (int c = 0; c < D / 16; ++c) *reinterpret_cast<uint4*>(v + c * 16) = make_uint4(0u, 0u, 0u, 0u);
-            } else if (u > vis) {
-              for (int c = 0; c < D / 4; ++c) {
-                uint32_t* p = reinterpret_cast<uint32_t*>(v + v_chunk<D>(t, c >> 2) * 16 + (c & 3) * 4);
-                const uint32_t nan = __vcmpeq4(*p & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-                if (!nan) continue;
-                *p &= ~nan;
+              for (int c = 0; c < D / 16; ++c) *reinterpret_cast<uint4*>(v + t * D + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            // 16 codes a thread of the rows vis + 1 .. L - 1 of this tile
+            for (int x = max(0, vis + 1 - tile * kTok) * (D / 16) + t; x < min(kTok, after) * (D / 16); x += 128) {
+              const int r = x / (D / 16), c = x % (D / 16);
+              uint4* p = reinterpret_cast<uint4*>(v + r * D + v_chunk<D>(r, c) * 16);
+              uint32_t y[4] = {p->x, p->y, p->z, p->w}, any = 0u;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) any |= __vcmpeq4(y[e] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+              if (any) {
+                for (int e = 0; e < 16; ++e) {
+                  const uint32_t code = 0x7Fu << (8 * (e & 3));
+                  if ((y[e >> 2] & code) != code) continue;
+                  y[e >> 2] &= ~(0xFFu << (8 * (e & 3)));
+                  atomicMin(&sh.nan_at[pb][c * 16 + e], tile * kTok + r);
+                }
                 sh.nan_any[pb] = 1;
-                for (int x = 0; x < 4; ++x)
-                  if (nan >> (8 * x) & 1u) atomicMin(&sh.nan_at[pb][c * 4 + x], u);
+                *p = make_uint4(y[0], y[1], y[2], y[3]);
               }
             }
           }
@@ -715,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const int et = max(max(sh.wev[wg][0], sh.wev[wg][1]), max(sh.wev[wg][2], sh.wev[wg][3]));
           uint8_t* pd = sP + wg * C::kP + (i * 2 * q / 16) * 2048 + (i * 2 * q % 16) + tok * 16;
-          const uint64_t c28 = pack2(28.f, 28.f);
+          const __half2 c28 = __floats2half2_rn(28.f, 28.f);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float cs = 448.f * c8_pow2(max(-126, ev[e] - et));
@@ -726,12 +798,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float2 x = unpack2(add2(z[e][j], mt[j]));
               const uint64_t p = pack2(ex2_approx(x.x), ex2_approx(x.y));
               ps[j] = add2(ps[j], p);
-              const uint64_t y2 = mul2(p, c2);
-              const float2 y = unpack2(y2);
-              p1[j] = c8_encode2(y.x, y.y);
-              const float2 f = c8_decode2(p1[j]);
-              const float2 r = unpack2(mul2(add2(y2, pack2(-f.x, -f.y)), c28));
-              p2[j] = c8_encode2(r.x, r.y);
+              const float2 y = unpack2(mul2(p, c2));
+              // Both terms from y rounded to fp16 (2^-11 of itself): the first's rest is exact there (a
+              // multiple of y's last bit, at most 2^-4 of it), and so is its 28-fold.
+              const __half2 h = __floats2half2_rn(y.x, y.y);
+              p1[j] = __nv_cvt_halfraw2_to_fp8x2(h, __NV_SATFINITE, __NV_E4M3);
+              const __half2_raw f = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)p1[j], __NV_E4M3);
+              p2[j] = __nv_cvt_halfraw2_to_fp8x2(__hmul2(__hsub2(h, __half2(f)), c28), __NV_SATFINITE, __NV_E4M3);
             }
             uint8_t* d = pd + e * 128;
             if constexpr (q == 8) {
@@ -755,7 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if ((lane >> 2) < q) sh.wsum_p[wg][q4][row0 + (lane >> 2)] = s;
           tc::mbar_arrive(&sh.p_full[wg]);
         }
-        st += 2;
+        st += kGroups;
         if (st >= C::kStages) {
           st -= C::kStages;
           ph ^= 1;
@@ -765,8 +838,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) tc::mbar_arrive(&sh.q_empty[pb]);
     }
   } else {
-    split_q<D, NR, W>(a, w, sh, sQ, warp - 11, 5, lane);
-    asm volatile("bar.arrive 4, 160;" ::: "memory");
+    const int q_first = warp - 4 - 4 * kGroups;
+    split_piece<D, NR, W>(a, w, sh, sQ, q_first, abort, lane);
     if constexpr (!W) {
     // ---- a thread per head dim: outputs ----
     const int q4 = warp & 3, t = tid & 127;
@@ -776,29 +849,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t o[C::kRowsT / 2];
 #pragma unroll
     for (int r = 0; r < C::kRowsT / 2; ++r) o[r] = 0ull;
-    float m_run = kNegMax, l = 0.f;  // row t's, in the first threads
-    int e_run = -126;
-    int k = 0;
-    for (; w.left > 0; walk_next(w, a)) {
+    int sb = 0;
+    uint32_t ph = 0;
+    for (Walk ahead = w; w.left > 0; w = ahead) {
+     walk_next(ahead, a);
+     if (ahead.left > 0) split_piece<D, NR, W>(a, ahead, sh, sQ, q_first, abort, lane);
      const int pb = w.piece & 1;
      const long unit = (long)w.b * units_b + w.g * a.nch + w.ch, slot = unit + blockIdx.x;
-     for (int n = w.t1 - w.t0; n > 0; --n, ++k) {
-      const int sb = k & 1;
-      warp_wait(&sh.p_full[sb], (uint32_t)((k >> 1) & 1), abort, a.status);
-      const int et = max(max(sh.wev[sb][0], sh.wev[sb][1]), max(sh.wev[sb][2], sh.wev[sb][3])), en = max(e_run, et);
-      if (t < NR) {
-        const float(&wm)[4][NR] = sh.wmax[sb];
-        const float(&ws)[4][NR] = sh.wsum_p[sb];
-        const float mt = fmaxf(fmaxf(wm[0][t], wm[1][t]), fmaxf(wm[2][t], wm[3][t])), mn = fmaxf(m_run, mt);
-        const float fa = ex2_approx(m_run - mn), fb = ex2_approx(mt - mn);
-        sh.acc_a[sb][t] = fa * c8_pow2(max(-126, e_run - en));
-        sh.acc_b[sb][t] = fb * c8_pow2(max(-126, et - en)) * (1.f / 448.f);
-        l = fmaf(l, fa, ((ws[0][t] + ws[1][t]) + (ws[2][t] + ws[3][t])) * fb);
-        m_run = mn;
-      }
-      e_run = en;
-      group_sync(3);
-      warp_wait(&sh.o_full[sb], (uint32_t)((k >> 1) & 1), abort, a.status);
+     for (int n = w.t1 - w.t0; n > 0; --n) {
+      warp_wait(&sh.f_full[sb], ph, abort, a.status);
+      warp_wait(&sh.o_full[sb], ph, abort, a.status);
       tc::fence_after_sync();
       const uint64_t c28 = pack2(1.f / 28.f, 1.f / 28.f);
 #pragma unroll
@@ -819,10 +879,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               x2 = __uint_as_float(c[0][x + q + 8]), y2 = __uint_as_float(c[0][x + q + 9]);
             }
           }
-          const int rr = rb + r0 + r;
-          const uint64_t fa = pack2(sh.acc_a[sb][rr], sh.acc_a[sb][rr + 1]);
-          const uint64_t fb = pack2(sh.acc_b[sb][rr], sh.acc_b[sb][rr + 1]);
-          o[(r0 + r) / 2] = fma2(o[(r0 + r) / 2], fa, mul2(fma2(pack2(x2, y2), c28, pack2(x1, y1)), fb));
+          const float4 f = sh.acc[sb][(rb + r0 + r) / 2];
+          o[(r0 + r) / 2] = fma2(o[(r0 + r) / 2], pack2(f.x, f.y),
+                                 mul2(fma2(pack2(x2, y2), c28, pack2(x1, y1)), pack2(f.z, f.w)));
         }
       }
       tc::fence_before_sync();
@@ -837,12 +896,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                              np <= w.L - a.n_new + (r0 + r + 1) / R ? nan : y.y);
           }
         }
-        group_sync(3);
+        group_sync(7);
         sh.nan_at[pb][t] = kNever;
         if (t == 0) sh.nan_any[pb] = 0;
       }
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sh.o_empty[sb]);
+      if (++sb == kGroups) {
+        sb = 0;
+        ph ^= 1u;
+      }
      }
         float* po = part.o(slot) + rb * D + dim;
 #pragma unroll
@@ -852,18 +915,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           po[(r + 1) * D] = y.y;
           o[r / 2] = 0ull;
         }
-        if (t < NR) {
-          part.m(slot)[t] = m_run;
-          part.l(slot)[t] = l;
-        }
         if (t == 0) {
-          *part.e(slot) = e_run;
           if (w.t0 == 0) part.first[unit] = (int)blockIdx.x;
           if (w.t1 == w.ntiles) part.last[unit] = (int)blockIdx.x;
         }
-        m_run = kNegMax;
-        l = 0.f;
-        e_run = -126;
     }
     }
   }
@@ -983,7 +1038,7 @@ template <int D, int NR, bool W>
 cudaError_t launch_main(const CUtensorMap& mk, const CUtensorMap& mv, C8AttendArgs a, int nch, int chunk_rows,
                         cudaStream_t s) {
   using C = Cfg<D, NR, W>;
-  constexpr int kSmem = C::kStages * C::kStage + 2 * C::kQ + 2 * C::kP + 1024;
+  constexpr int kSmem = C::kStages * C::kStage + 2 * C::kQ + C::kGroups * C::kP + 1024;
   cudaError_t e = cudaFuncSetAttribute(cache8_attend_kernel<D, NR, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   a.nch = nch;
@@ -991,7 +1046,7 @@ cudaError_t launch_main(const CUtensorMap& mk, const CUtensorMap& mv, C8AttendAr
   a.block_log2 = a.block == 8 ? 3 : a.block == 16 ? 4 : a.block == 32 ? 5 : a.block == 64 ? 6 : 7;
   const long tiles = (long)a.batch * a.G * nch * ((a.T + kTok - 1) / kTok);
   const unsigned grid = (unsigned)(tiles < kGridMax ? tiles : kGridMax);
-  cache8_attend_kernel<D, NR, W><<<grid, kThreads, kSmem, s>>>(mk, mv, a);
+  cache8_attend_kernel<D, NR, W><<<grid, C::kThreads, kSmem, s>>>(mk, mv, a);
   return cudaGetLastError();
 }
 
