@@ -204,6 +204,12 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
   return r;
 }
+// True in one lane of the warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.b32 %0, 1, 0, p; }" : "=r"(p));
+  return p != 0;
+}
 // pairs of fp32
 __device__ __forceinline__ uint64_t pack2(float x, float y) {
   uint64_t r;
@@ -497,25 +503,20 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
         tc::mbar_wait(&sh.full[i % C::kStages], (uint32_t)((i / C::kStages) & 1), &none);
     }
   } else if (warp == 1) {
-    // ---- MMAs of S^T ----
-    if (lane == 0) {
-      constexpr uint32_t id_s = idesc_f8(C::N, false, false);
-      const uint64_t dk = tc::smem_desc_kmajor(sKV, D), dq = tc::smem_desc_kmajor_noswz(sQ, 128, D * 8);
-      volatile int none = 0;
-      int k = 0, st = 0, sb = 0;
-      uint32_t ph = 0, sph = 1;  // phases of the stages and of S^T's buffers
-      bool ok = true;
-      for (; w.left > 0 && ok; walk_next(w, a)) {
-        const int pb = w.piece & 1;
-        const uint64_t db = dq + (uint32_t)(pb * (C::kQ >> 4));
-        ok = tc::mbar_wait(&sh.q_full[pb], (uint32_t)((w.piece >> 1) & 1), abort, a.status);
-        for (int n = w.t1 - w.t0; n > 0 && ok; --n, ++k) {
-          if (!tc::mbar_wait(&sh.full[st], ph, abort, a.status) ||
-              (k >= kGroups && !tc::mbar_wait(&sh.s_empty[sb], sph, abort, a.status))) {
-            ok = false;
-            break;
-          }
-          tc::fence_after_sync();
+    // ---- MMAs of S^T: the warp waits, one lane issues ----
+    constexpr uint32_t id_s = idesc_f8(C::N, false, false);
+    const uint64_t dk = tc::smem_desc_kmajor(sKV, D), dq = tc::smem_desc_kmajor_noswz(sQ, 128, D * 8);
+    int k = 0, st = 0, sb = 0;
+    uint32_t ph = 0, sph = 1;  // phases of the stages and of S^T's buffers
+    for (; w.left > 0; walk_next(w, a)) {
+      const int pb = w.piece & 1;
+      const uint64_t db = dq + (uint32_t)(pb * (C::kQ >> 4));
+      warp_wait(&sh.q_full[pb], (uint32_t)((w.piece >> 1) & 1), abort, a.status);
+      for (int n = __shfl_sync(0xFFFFFFFFu, w.t1 - w.t0, 0); n > 0; --n, ++k) {
+        warp_wait(&sh.full[st], ph, abort, a.status);
+        if (k >= kGroups) warp_wait(&sh.s_empty[sb], sph, abort, a.status);
+        tc::fence_after_sync();
+        if (elect_one()) {
           const uint64_t da = dk + (uint32_t)(st * (C::kStage >> 4));
 #pragma unroll
           for (int kk = 0; kk < D / 32; ++kk)
@@ -523,64 +524,65 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
           tc::mma_commit(&sh.s_full[sb]);
           if (W) tc::mma_commit(&sh.empty[st]);
           if (n == 1) tc::mma_commit(&sh.q_empty[pb]);
-          if (++sb == kGroups) {
-            sb = 0;
-            sph ^= 1u;
-          }
-          if (++st == C::kStages) {
-            st = 0;
-            ph ^= 1;
-          }
+        }
+        __syncwarp();
+        if (++sb == kGroups) {
+          sb = 0;
+          sph ^= 1u;
+        }
+        if (++st == C::kStages) {
+          st = 0;
+          ph ^= 1;
         }
       }
-      if (!ok) {
-        if (!*abort) report(a.status, SGQA_ERR_TIMEOUT);
-        *abort = 1;
-      }
-      // the MMAs in flight end before the CTA leaves
-      if (k > 0) tc::mbar_wait(&sh.s_full[(k - 1) % kGroups], (uint32_t)(((k - 1) / kGroups) & 1), &none);
-      if (W && ok)
+    }
+    // the MMAs in flight end before the CTA leaves
+    if (lane == 0) {
+      volatile int none = 0;
+      tc::mbar_wait(&sh.s_full[(k - 1) % kGroups], (uint32_t)(((k - 1) / kGroups) & 1), &none);
+      if (W)
         for (int j = max(0, k - C::kStages); j < k; ++j)
           tc::mbar_wait(&sh.empty[j % C::kStages], (uint32_t)((j / C::kStages) & 1), abort);
-      if (ok) tc::mbar_wait(&sh.q_empty[(w.piece - 1) & 1], (uint32_t)(((w.piece - 1) >> 1) & 1), abort);
+      tc::mbar_wait(&sh.q_empty[(w.piece - 1) & 1], (uint32_t)(((w.piece - 1) >> 1) & 1), abort);
     }
   } else if (warp == 2) {
     // ---- MMAs of O^T (no such in the weights' pass, where this warp splits q too) ----
     if constexpr (W) {
       split_all<D, NR, W>(a, w, sh, sQ, 1, abort, lane);
-    } else if (lane == 0) {
+    } else {
       constexpr uint32_t id_o = idesc_f8(C::N, true, true);
       const uint64_t dv = D == 128 ? tc::smem_desc_mnmajor_sw128(sKV + C::kTile, 1024, 1024)
                                    : smem_desc_mnmajor_sw64_twice(sKV + C::kTile);
       // P: [16 columns][128 tokens][16 bytes]: 8 tokens are 128 bytes, 16 columns 2048
       const uint64_t dp = tc::smem_desc_kmajor_noswz(sP, 128, 2048);
-      volatile int none = 0;
-      const int count = w.left;
-      int k = 0, st = 0, pb = 0;
+      const int count = __shfl_sync(0xFFFFFFFFu, w.left, 0);
+      int st = 0, pb = 0;
       uint32_t ph = 0;
-      for (; k < count; ++k) {
-        if (!tc::mbar_wait(&sh.p_full[pb], ph, abort, a.status) ||
-            (k >= kGroups && !tc::mbar_wait(&sh.o_empty[pb], ph ^ 1u, abort, a.status))) {
-          if (!*abort) report(a.status, SGQA_ERR_TIMEOUT);
-          *abort = 1;
-          break;
-        }
+      for (int k = 0; k < count; ++k) {
+        warp_wait(&sh.p_full[pb], ph, abort, a.status);
+        if (k >= kGroups) warp_wait(&sh.o_empty[pb], ph ^ 1u, abort, a.status);
         tc::fence_after_sync();
-        const uint64_t da = dv + (uint32_t)(st * (C::kStage >> 4)), db = dp + (uint32_t)(pb * (C::kP >> 4));
+        if (elect_one()) {
+          const uint64_t da = dv + (uint32_t)(st * (C::kStage >> 4)), db = dp + (uint32_t)(pb * (C::kP >> 4));
 #pragma unroll
-        for (int kk = 0; kk < kTok / 32; ++kk)
-          mma_f8(tmem_o + (uint32_t)(pb * C::N), da + kk * (32 * D >> 4), db + kk * 32, id_o, kk > 0);
-        tc::mma_commit(&sh.empty[st]);
-        tc::mma_commit(&sh.o_full[pb]);
+          for (int kk = 0; kk < kTok / 32; ++kk)
+            mma_f8(tmem_o + (uint32_t)(pb * C::N), da + kk * (32 * D >> 4), db + kk * 32, id_o, kk > 0);
+          tc::mma_commit(&sh.empty[st]);
+          tc::mma_commit(&sh.o_full[pb]);
+        }
+        __syncwarp();
         if (++st == C::kStages) st = 0;
         if (++pb == kGroups) {
           pb = 0;
           ph ^= 1u;
         }
       }
-      if (k > 0) tc::mbar_wait(&sh.o_full[(k - 1) % kGroups], (uint32_t)(((k - 1) / kGroups) & 1), &none);
-      for (int j = max(0, k - C::kStages); j < k; ++j)
-        tc::mbar_wait(&sh.empty[j % C::kStages], (uint32_t)((j / C::kStages) & 1), &none);
+      if (lane == 0) {
+        volatile int none = 0;
+        tc::mbar_wait(&sh.o_full[(count - 1) % kGroups], (uint32_t)(((count - 1) / kGroups) & 1), &none);
+        for (int j = max(0, count - C::kStages); j < count; ++j)
+          tc::mbar_wait(&sh.empty[j % C::kStages], (uint32_t)((j / C::kStages) & 1), &none);
+      }
     }
   } else if (warp == 3) {
     if constexpr (W) {
