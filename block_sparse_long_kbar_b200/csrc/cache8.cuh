@@ -126,6 +126,11 @@ __device__ __forceinline__ uint32_t c8_max_u16x2(uint32_t x, uint32_t y) {
   return r;
 }
 
+// A kernel launched with programmatic serialization starts when every CTA of the one before it has
+// called grid_dependents() or ended; grid_wait() returns when that kernel has ended and its writes are seen.
+__device__ __forceinline__ void grid_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // lens[b] if it is a length this cache can have, else 0 and a device check
 __device__ __forceinline__ int c8_len(const int32_t* lens, int b, int T, int* status) {
   const int n = __ldg(lens + b);

@@ -69,7 +69,7 @@ struct Shared {
   uint32_t tmem;
   volatile int abort_flag;
   int start_b, start_off;
-  int wsum[32];
+  int wsum[32], wmore[32];
   int nan_any[2];
   int nan_at[2][128];                      // per head dim: first token not visible to all rows whose V is NaN there
   int wev[kMaxGroups][4];
@@ -258,6 +258,15 @@ __device__ __forceinline__ void warp_wait(uint64_t* bar, uint32_t parity, volati
   __syncwarp();
 }
 
+__device__ __forceinline__ int warp_scan(int x, int lane) {
+#pragma unroll
+  for (int h = 1; h < 32; h <<= 1) {
+    const int y = __shfl_up_sync(0xFFFFFFFFu, x, h);
+    if (lane >= h) x += y;
+  }
+  return x;
+}
+
 // x[j] over the eight lanes that share rows (lane / 4), joined by op in a fixed order; the lane gets
 // row (lane / 4) mod Q.
 template <int Q, class Op>
@@ -362,7 +371,7 @@ __device__ __forceinline__ void split_q(const C8AttendArgs& a, const Walk& w, Sh
   tc::fence_proxy_async();
 }
 
-// One of the warps that split q: rows first, first + kQWarps, .. of the piece w, and of all pieces.
+// One of the warps that split q: rows first, first + kQWarps, .. of the piece w, and of all later ones.
 template <int D, int NR, bool W>
 __device__ __forceinline__ void split_piece(const C8AttendArgs& a, const Walk& w, Shared<NR>& sh, uint8_t* sQ, int first,
                                             volatile int* abort, int lane) {
@@ -374,7 +383,7 @@ __device__ __forceinline__ void split_piece(const C8AttendArgs& a, const Walk& w
 template <int D, int NR, bool W>
 __device__ __forceinline__ void split_all(const C8AttendArgs& a, Walk w, Shared<NR>& sh, uint8_t* sQ, int first,
                                           volatile int* abort, int lane) {
-  for (; w.left > 0; walk_next(w, a)) split_piece<D, NR, W>(a, w, sh, sQ, first, abort, lane);
+  for (walk_next(w, a); w.left > 0; walk_next(w, a)) split_piece<D, NR, W>(a, w, sh, sQ, first, abort, lane);
 }
 
 template <int D, int NR, bool W>
@@ -391,70 +400,78 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int units_b = a.G * a.nch;
 
-  // ---- this CTA's piece of the tiles ----
-  int sum = 0;
-  for (int b = tid; b < a.batch; b += kThreads) sum += tiles_of(c8_len(a.lens, b, a.T, a.status)) * units_b;
-  sum = __reduce_add_sync(0xFFFFFFFFu, sum);
-  if (lane == 0) sh.wsum[warp] = sum;
-  if (tid == 0) {
-    for (int i = 0; i < 8; ++i) {
-      tc::mbar_init(&sh.full[i], 1 + 32);
-      tc::mbar_init(&sh.empty[i], W ? 1 + 4 : 1);  // the weights' pass reads scales after the MMA
-    }
-    for (int i = 0; i < kGroups; ++i) {
-      tc::mbar_init(&sh.s_full[i], 1);
-      tc::mbar_init(&sh.s_empty[i], 4);
-      tc::mbar_init(&sh.p_full[i], 128);
-      tc::mbar_init(&sh.f_full[i], 32);
-      tc::mbar_init(&sh.o_full[i], 1);
-      tc::mbar_init(&sh.o_empty[i], 4);
-    }
-    for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&sh.q_full[i], 32 * C::kQWarps);
-      tc::mbar_init(&sh.q_empty[i], 1 + 4 * kGroups);
-      sh.nan_any[i] = 0;
-    }
+  grid_dependents();  // (the kernels behind wait for this one's end where they need it)
+  // ---- barriers; this CTA's piece of the tiles ----
+  if (tid < 8) {
+    tc::mbar_init(&sh.full[tid], 1 + 32);
+    tc::mbar_init(&sh.empty[tid], W ? 1 + 4 : 1);  // the weights' pass reads scales after the MMA
+  } else if (tid < 8 + kGroups) {
+    const int i = tid - 8;
+    tc::mbar_init(&sh.s_full[i], 1);
+    tc::mbar_init(&sh.s_empty[i], 4);
+    tc::mbar_init(&sh.p_full[i], 128);
+    tc::mbar_init(&sh.f_full[i], 32);
+    tc::mbar_init(&sh.o_full[i], 1);
+    tc::mbar_init(&sh.o_empty[i], 4);
+  } else if (tid >= 16 && tid < 18) {
+    tc::mbar_init(&sh.q_full[tid - 16], 32 * C::kQWarps);
+    tc::mbar_init(&sh.q_empty[tid - 16], 1 + 4 * kGroups);
+    sh.nan_any[tid - 16] = 0;
     sh.abort_flag = 0;
-    tc::fence_mbar_init();
+  } else if (tid == 32) {
     tc::prefetch_tensormap(&map_k);
     if (!W) tc::prefetch_tensormap(&map_v);
   }
+  if (tid < 18) tc::fence_mbar_init();
   if (tid < 256) sh.nan_at[tid >> 7][tid & 127] = kNever;
+  // tiles of the first kThreads sequences, a thread each, and of all others
+  const int mine = tid < a.batch ? tiles_of(c8_len(a.lens, tid, a.T, a.status)) * units_b : 0;
+  int more = 0;
+  for (int b = tid + kThreads; b < a.batch; b += kThreads) more += tiles_of(c8_len(a.lens, b, a.T, a.status)) * units_b;
+  more = __reduce_add_sync(0xFFFFFFFFu, more);
+  int upto = warp_scan(mine, lane);
+  if (lane == 31) {
+    sh.wsum[warp] = upto;
+    sh.wmore[warp] = more;
+  }
   __syncthreads();
-  int total = 0;
+  int total = 0, seen = 0;
 #pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) total += sh.wsum[i];
+  for (int i = 0; i < kThreads / 32; ++i) {
+    if (i < warp) upto += sh.wsum[i];
+    seen += sh.wsum[i];
+    total += sh.wmore[i];
+  }
+  total += seen;
   // (every CTA below n has a tile: the CTAs between a unit's first and last have all written)
   const int n = min((int)gridDim.x, total), cta = (int)blockIdx.x;
-  if (cta >= n) return;
-  const int t0 = (int)((long)total * cta / n), t1 = (int)((long)total * (cta + 1) / n);
-  __syncthreads();
-  for (int b0 = 0, run = 0; b0 < a.batch; b0 += kThreads) {
-    const int b = b0 + tid;
-    const int nb = b < a.batch ? tiles_of(len_of(a, b)) * units_b : 0;
-    int x = nb;
-#pragma unroll
-    for (int h = 1; h < 32; h <<= 1) {
-      const int y = __shfl_up_sync(0xFFFFFFFFu, x, h);
-      if (lane >= h) x += y;
-    }
+  if (cta >= n) {
+    if (W) grid_wait();  // (no kernel ends before the one it was started behind)
+    return;
+  }
+  const int each = total / n, odd = total - each * n;
+  const int t0 = each * cta + min(cta, odd), t1 = t0 + each + (cta < odd ? 1 : 0);
+  if (warp == 1) tc::tmem_alloc(&sh.tmem, C::kTmem);
+  if (upto > t0 && upto - mine <= t0) {
+    sh.start_b = tid;
+    sh.start_off = t0 - (upto - mine);
+  }
+  for (int b0 = kThreads; seen <= t0; b0 += kThreads) {
+    const int b = b0 + tid, nb = b < a.batch ? tiles_of(len_of(a, b)) * units_b : 0;
+    int x = warp_scan(nb, lane);
+    __syncthreads();
     if (lane == 31) sh.wsum[warp] = x;
     __syncthreads();
-    int all = 0;
-#pragma unroll
+    x += seen;
     for (int i = 0; i < kThreads / 32; ++i) {
       if (i < warp) x += sh.wsum[i];
-      all += sh.wsum[i];
+      seen += sh.wsum[i];
     }
-    if (run + x > t0 && run + x - nb <= t0) {
+    if (x > t0 && x - nb <= t0) {
       sh.start_b = b;
-      sh.start_off = t0 - (run + x - nb);
+      sh.start_off = t0 - (x - nb);
     }
-    run += all;
-    __syncthreads();
-    if (run > t0) break;
   }
-  if (warp == 1) tc::tmem_alloc(&sh.tmem, C::kTmem);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -465,6 +482,18 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
   walk_begin(w, a, sh.start_b, sh.start_off, t1 - t0);
   const Part<D, NR> part(a.part, (long)a.batch * units_b);
 
+  // the first piece's rows of q: all warps but those that have tiles to fetch and to multiply
+  constexpr int kQFirst = W ? 2 : 4 + 4 * kGroups;  // the warps that split the later pieces' rows
+  if (warp >= 2) {
+    if (W) grid_wait();  // the rows' sums, and what the weights so far were written by
+    split_q<D, NR, W>(a, w, sh, sQ, warp - 2, kThreads / 32 - 2, lane);
+    if (warp >= kQFirst && warp < kQFirst + C::kQWarps) {
+      asm volatile("bar.sync 8, %0;" ::"n"(kThreads - 64) : "memory");
+      tc::mbar_arrive(&sh.q_full[0]);
+    } else {
+      asm volatile("bar.arrive 8, %0;" ::"n"(kThreads - 64) : "memory");
+    }
+  }
   if (warp == 0) {
     // ---- TMA: K and V tiles; a lane per block: their scales ----
     const long nblk = ((long)a.T + a.block - 1) >> a.block_log2;
@@ -545,11 +574,11 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
           tc::mbar_wait(&sh.empty[j % C::kStages], (uint32_t)((j / C::kStages) & 1), abort);
       tc::mbar_wait(&sh.q_empty[(w.piece - 1) & 1], (uint32_t)(((w.piece - 1) >> 1) & 1), abort);
     }
+  } else if (W && warp < 4) {
+    split_all<D, NR, W>(a, w, sh, sQ, warp - 2, abort, lane);
   } else if (warp == 2) {
-    // ---- MMAs of O^T (no such in the weights' pass, where this warp splits q too) ----
-    if constexpr (W) {
-      split_all<D, NR, W>(a, w, sh, sQ, 1, abort, lane);
-    } else {
+    // ---- MMAs of O^T ----
+    {
       constexpr uint32_t id_o = idesc_f8(C::N, true, true);
       const uint64_t dv = D == 128 ? tc::smem_desc_mnmajor_sw128(sKV + C::kTile, 1024, 1024)
                                    : smem_desc_mnmajor_sw64_twice(sKV + C::kTile);
@@ -585,9 +614,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
       }
     }
   } else if (warp == 3) {
-    if constexpr (W) {
-      split_all<D, NR, W>(a, w, sh, sQ, 0, abort, lane);
-    } else {
+    {
       // ---- a lane per row: running maxima, denominators, factors for the accumulating warps ----
       float m_run = kNegMax, l = 0.f;
       int e_run = -126, sb = 0;
@@ -841,7 +868,6 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
     }
   } else {
     const int q_first = warp - 4 - 4 * kGroups;
-    split_piece<D, NR, W>(a, w, sh, sQ, q_first, abort, lane);
     if constexpr (!W) {
     // ---- a thread per head dim: outputs ----
     const int q4 = warp & 3, t = tid & 127;
@@ -932,80 +958,121 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
   }
 }
 
-// Joins the pieces of a unit in the order of their tiles: a CTA per (sequence, group, row). The
-// factors of 256 pieces at a time are made by a thread each, then warps take the pieces in turn.
-constexpr int kJoinThr = 256;
-template <int D, int NR>
-__global__ void __launch_bounds__(kJoinThr) cache8_join_kernel(C8AttendArgs a) {
+// Joins the pieces of a unit: PER warps per (sequence, group, row), which take its pieces in turn; a
+// lane per piece for the factors, per D / 32 head dims for the sums. The order is fixed.
+constexpr int kJoinWarps = 8;
+template <int D, int NR, int PER>
+__global__ void __launch_bounds__(kJoinWarps * 32) cache8_join_kernel(C8AttendArgs a) {
   constexpr int kV = D / 32;
-  __shared__ float s_f[kJoinThr], s_o[kJoinThr / 32][D], s_m[kJoinThr / 32], s_l[kJoinThr / 32];
-  __shared__ int s_e[kJoinThr / 32];
+  __shared__ float s_m[kJoinWarps], s_l[kJoinWarps], s_o[PER > 1 ? kJoinWarps : 1][D];
+  __shared__ int s_e[kJoinWarps];
+  grid_dependents();
+  grid_wait();
   if (tc::grid_timed_out(a.status)) return;
-  const int R = a.Hq / a.G, rows = a.n_new * R;
-  const int gr = blockIdx.x % rows, bg = blockIdx.x / rows, b = bg / a.G, g = bg % a.G;
-  const int r = gr % a.chunk_rows, t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const int R = a.Hq / a.G, rows = a.n_new * R, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int item = (blockIdx.x * kJoinWarps + warp) / PER, part_of = warp % PER;
+  if (item >= a.batch * a.G * rows) return;
+  const int gr = item % rows, bg = item / rows, b = bg / a.G, g = bg % a.G;
+  const int r = gr % a.chunk_rows;
   const long unit = (long)bg * a.nch + gr / a.chunk_rows;
-  const int L = len_of(a, b);
   const Part<D, NR> part(a.part, (long)a.batch * a.G * a.nch);
-  const long at = (((long)b * a.n_new + gr / R) * a.Hq + (long)g * R + gr % R) * D;
-  const bool some = L > a.n_new - 1 - gr / R;
-  const int c0 = some ? part.first[unit] : 0, n = some ? part.last[unit] - c0 + 1 : 0;
+  const long at = (((long)b * a.n_new + gr / R) * a.Hq + (long)g * R + gr % R) * D + lane * kV;
+  uint32_t gate[kV / 2];
+#pragma unroll
+  for (int v = 0; v < kV / 2; ++v) gate[v] = __ldg(reinterpret_cast<const uint32_t*>(a.gate + at) + v);
+  const int c0 = part.first[unit], c1 = part.last[unit];  // (read before it is known that there are such)
+  const bool some = len_of(a, b) > a.n_new - 1 - gr / R;
+  const int n = some ? c1 - c0 + 1 : 0;  // pieces; this warp's are part_of, part_of + PER, ..
   float m = kNegMax, den = 0.f, o[kV];
   int e = -126;
 #pragma unroll
-  for (int x = 0; x < kV; ++x) o[x] = 0.f;
-  for (int c = t; c < n; c += kJoinThr) {
-    m = fmaxf(m, part.m(unit + c0 + c)[r]);
-    e = max(e, *part.e(unit + c0 + c));
-  }
+  for (int v = 0; v < kV; ++v) o[v] = 0.f;
+  for (int p0 = part_of; p0 < n; p0 += 32 * PER) {
+    const long slot = unit + c0 + p0 + lane * PER;
+    const bool has = p0 + lane * PER < n;
+    const float pm = has ? part.m(slot)[r] : kNegMax, pl = has ? part.l(slot)[r] : 0.f;
+    const int pe = has ? *part.e(slot) : -126;
+    // the sums so far and these pieces' on common references
+    float mn = fmaxf(m, pm);
 #pragma unroll
-  for (int h = 16; h; h >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, h));
-  e = __reduce_max_sync(0xFFFFFFFFu, e);
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_e[warp] = e;
-  }
-  __syncthreads();
+    for (int h = 16; h; h >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, h));
+    const int en = max(e, __reduce_max_sync(0xFFFFFFFFu, pe));
+    const float old = ex2_approx(m - mn), f = ex2_approx(pm - mn);
+    float l = pl * f;
 #pragma unroll
-  for (int x = 0; x < kJoinThr / 32; ++x) {
-    m = fmaxf(m, s_m[x]);
-    e = max(e, s_e[x]);
-  }
-  for (int p0 = 0; p0 < n; p0 += kJoinThr) {
-    const int c = p0 + t;
-    if (c < n) {
-      const long slot = unit + c0 + c;
-      const float f = ex2_approx(part.m(slot)[r] - m);
-      s_f[t] = f * c8_pow2(max(-126, *part.e(slot) - e));
-      den = fmaf(part.l(slot)[r], f, den);
+    for (int h = 16; h; h >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, h);
+    den = fmaf(den, old, l);
+    const float fe = f * c8_pow2(max(-126, pe - en)), olde = old * c8_pow2(max(-126, e - en));
+#pragma unroll
+    for (int v = 0; v < kV; ++v) o[v] *= olde;
+    m = mn;
+    e = en;
+    const float* src = part.o(unit + c0 + p0) + r * D + lane * kV;
+    const int last = min(32, (n - p0 + PER - 1) / PER);
+#pragma unroll 8
+    for (int x = 0; x < last; ++x) {
+      const float fx = __shfl_sync(0xFFFFFFFFu, fe, x);
+      const float* y = src + (long)x * PER * Part<D, NR>::kRec;
+#pragma unroll
+      for (int v = 0; v < kV; v += 2) {
+        const float2 y2 = *reinterpret_cast<const float2*>(y + v);
+        o[v] = fmaf(y2.x, fx, o[v]);
+        o[v + 1] = fmaf(y2.y, fx, o[v + 1]);
+      }
     }
-    __syncthreads();
-#pragma unroll 4
-    for (int x = warp; x < min(kJoinThr, n - p0); x += kJoinThr / 32) {
-      const float* src = part.o(unit + c0 + p0 + x) + r * D + lane * kV;
-      const float f = s_f[x];
-#pragma unroll
-      for (int v = 0; v < kV; ++v) o[v] = fmaf(src[v], f, o[v]);
+  }
+  if constexpr (PER > 1) {
+    if (lane == 0) {
+      s_m[warp] = m;
+      s_e[warp] = e;
+      s_l[warp] = den;
     }
-    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < kV; ++v) s_o[warp][lane * kV + v] = o[v];
+    __syncthreads();  // (all warps of the CTA have the same item)
+    if (warp > 0) return;
+    for (int x = 1; x < PER; ++x) {
+      m = fmaxf(m, s_m[x]);
+      e = max(e, s_e[x]);
+    }
+    den = 0.f;
+#pragma unroll
+    for (int v = 0; v < kV; ++v) o[v] = 0.f;
+#pragma unroll
+    for (int x = 0; x < PER; ++x) {
+      const float f = ex2_approx(s_m[x] - m), fe = f * c8_pow2(max(-126, s_e[x] - e));
+      den = fmaf(s_l[x], f, den);
+#pragma unroll
+      for (int v = 0; v < kV; ++v) o[v] = fmaf(s_o[x][lane * kV + v], fe, o[v]);
+    }
   }
+  const float scale = c8_pow2(e);
 #pragma unroll
-  for (int h = 16; h; h >>= 1) den += __shfl_xor_sync(0xFFFFFFFFu, den, h);
-  if (lane == 0) s_l[warp] = den;
-#pragma unroll
-  for (int v = 0; v < kV; ++v) s_o[warp][lane * kV + v] = o[v];
-  __syncthreads();
-  den = 0.f;
-#pragma unroll
-  for (int x = 0; x < kJoinThr / 32; ++x) den += s_l[x];
-  if (t < D) {
-    float num = 0.f;
-#pragma unroll
-    for (int x = 0; x < kJoinThr / 32; ++x) num += s_o[x][t];
-    const float y = den == 0.f ? 0.f : num / den * c8_pow2(e);
-    a.out[at + t] = f32_to_bf16_rne(y * sigmoid_fast(bf16_to_f32(__ldg(a.gate + at + t))));
+  for (int v = 0; v < kV; v += 2) {
+    const float y0 = den == 0.f ? 0.f : o[v] / den * scale, y1 = den == 0.f ? 0.f : o[v + 1] / den * scale;
+    const uint32_t gt = gate[v / 2];
+    reinterpret_cast<uint32_t*>(a.out + at)[v / 2] =
+        f32_to_bf16_rne(y0 * sigmoid_fast(bf16_lo(gt))) | ((uint32_t)f32_to_bf16_rne(y1 * sigmoid_fast(bf16_hi(gt))) << 16);
   }
-  if (t == 0 && a.w_out) a.lse[(long)bg * rows + gr] = den == 0.f ? 0.f : m + log2f(den);
+  if (lane == 0 && a.w_out) a.lse[item] = den == 0.f ? 0.f : m + log2f(den);
+}
+
+// Launch whose start overlaps the end of the kernel before it on the stream (after which it waits
+// where it needs that kernel's results) or, with ahead false, an ordinary one.
+template <class... P, class... A>
+cudaError_t launch_behind(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t s, bool ahead,
+                          A... args) {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &at;
+  cfg.numAttrs = ahead ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -1048,8 +1115,7 @@ cudaError_t launch_main(const CUtensorMap& mk, const CUtensorMap& mv, C8AttendAr
   a.block_log2 = a.block == 8 ? 3 : a.block == 16 ? 4 : a.block == 32 ? 5 : a.block == 64 ? 6 : 7;
   const long tiles = (long)a.batch * a.G * nch * ((a.T + kTok - 1) / kTok);
   const unsigned grid = (unsigned)(tiles < kGridMax ? tiles : kGridMax);
-  cache8_attend_kernel<D, NR, W><<<grid, C::kThreads, kSmem, s>>>(mk, mv, a);
-  return cudaGetLastError();
+  return launch_behind(cache8_attend_kernel<D, NR, W>, grid, C::kThreads, kSmem, s, W, mk, mv, a);
 }
 
 // rows of a unit: all of a (sequence, group), or halves of them
@@ -1068,10 +1134,15 @@ cudaError_t launch_rows(const CUtensorMap& mk, const CUtensorMap& mv, C8AttendAr
   a.nch = rw.nch;
   a.chunk_rows = rw.chunk_rows;
   const int rows = a.n_new * (a.Hq / a.G);
-  const long ctas = (long)a.batch * a.G * rows;
-  if (ctas > 0x7FFFFFFFL) return cudaErrorInvalidConfiguration;
-  cache8_join_kernel<D, NR><<<(unsigned)ctas, kJoinThr, 0, s>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess || !a.w_out) return e;
+  const long items = (long)a.batch * a.G * rows;
+  if (items > 0x7FFFFFF0L) return cudaErrorInvalidConfiguration;
+  // eight warps a row while that is a wave of CTAs (a long sequence's rows have many pieces), else one
+  if (items <= 148 * 8)
+    e = launch_behind(cache8_join_kernel<D, NR, kJoinWarps>, (unsigned)items, kJoinWarps * 32, 0, s, true, a);
+  else
+    e = launch_behind(cache8_join_kernel<D, NR, 1>, (unsigned)((items + kJoinWarps - 1) / kJoinWarps), kJoinWarps * 32, 0,
+                      s, true, a);
+  if (e != cudaSuccess || !a.w_out) return e;
   return rw.nch == 1 ? launch_main<D, NR, true>(mk, mv, a, 1, rows, s) : launch_main<D, 64, true>(mk, mv, a, 1, rows, s);
 }
 template <int D>
