@@ -78,8 +78,11 @@ struct Shared {
   int lim[2][NR];                          // a row's own position; -1: no row
   alignas(16) float wmax[kMaxGroups][4][NR];    // per softmax group and warp: a row's maximum over the tile
   alignas(16) float wsum_p[kMaxGroups][4][NR];  // and the sum of its probabilities
-  // per softmax group: factors of the sums so far (x, y) and of this tile (z, w) for pairs of rows
-  float4 acc[kMaxGroups][NR / 2];
+  // per softmax group, for the accumulating warps: factors of the sums so far, and whether any is not 1;
+  // of this tile's first (x, y) and second (z, w) terms for pairs of rows
+  alignas(16) float fa[kMaxGroups][NR];
+  int any_fa[kMaxGroups];
+  float4 fb[kMaxGroups][NR / 2];
 };
 
 // The tiles of one CTA in order, a piece of a unit at a time: tiles [t0, t1) of unit ((sequence b,
@@ -622,19 +625,25 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
       for (; w.left > 0; walk_next(w, a)) {
         for (int n = w.t1 - w.t0; n > 0; --n) {
           warp_wait(&sh.p_full[sb], ph, abort, a.status);
+          float now = 1.f;
           const int et = max(max(sh.wev[sb][0], sh.wev[sb][1]), max(sh.wev[sb][2], sh.wev[sb][3])), en = max(e_run, et);
           if (lane < NR) {
             const float(&wm)[4][NR] = sh.wmax[sb];
             const float(&ws)[4][NR] = sh.wsum_p[sb];
             const float mt = fmaxf(fmaxf(wm[0][lane], wm[1][lane]), fmaxf(wm[2][lane], wm[3][lane]));
             const float mn = fmaxf(m_run, mt), fa = ex2_approx(m_run - mn), fb = ex2_approx(mt - mn);
-            float* f = reinterpret_cast<float*>(&sh.acc[sb][lane >> 1]) + (lane & 1);
-            f[0] = fa * c8_pow2(max(-126, e_run - en));
-            f[2] = fb * c8_pow2(max(-126, et - en)) * (1.f / 448.f);
+            const float b = fb * c8_pow2(max(-126, et - en)) * (1.f / 448.f);
+            float* f = reinterpret_cast<float*>(&sh.fb[sb][lane >> 1]) + (lane & 1);
+            f[0] = b;
+            f[2] = b * (1.f / 28.f);
+            now = fa * c8_pow2(max(-126, e_run - en));
+            sh.fa[sb][lane] = now;
             l = fmaf(l, fa, ((ws[0][lane] + ws[1][lane]) + (ws[2][lane] + ws[3][lane])) * fb);
             m_run = mn;
           }
           e_run = en;
+          const bool any = __any_sync(0xFFFFFFFFu, now != 1.f);
+          if (lane == 0) sh.any_fa[sb] = any;
           tc::mbar_arrive(&sh.f_full[sb]);
           if (++sb == kGroups) {
             sb = 0;
@@ -685,12 +694,28 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
         tc::fence_after_sync();
         float sk[4];
         int ev[4], we = -127;
+        const int sb = tok >> a.block_log2;
+        sk[0] = sh.scale[st][sb];
+        ev[0] = W ? 0 : (int)(__float_as_uint(sh.scale[st][16 + sb]) >> 23 & 255u) - 127;
+#pragma unroll
+        for (int e = 1; e < 4; ++e) {
+          sk[e] = sk[0];
+          ev[e] = ev[0];
+        }
+        if (a.block_log2 < 5) {  // else a lane's four tokens, all within 32, are in one block
+#pragma unroll
+          for (int e = 1; e < 4; ++e) {
+            const int sb = (tok + 8 * e) >> a.block_log2;
+            sk[e] = sh.scale[st][sb];
+            ev[e] = W ? 0 : (int)(__float_as_uint(sh.scale[st][16 + sb]) >> 23 & 255u) - 127;
+          }
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const bool live = !edge || u0 + 8 * e < w.L;
-          const int sb = (tok + 8 * e) >> a.block_log2;
-          sk[e] = live ? sh.scale[st][sb] : 0.f;
-          ev[e] = !W && live ? (int)(__float_as_uint(sh.scale[st][16 + sb]) >> 23 & 255u) - 127 : -127;
+          if (edge && u0 + 8 * e >= w.L) {  // whatever lies behind the last token
+            sk[e] = 0.f;
+            ev[e] = -127;
+          }
           we = max(we, ev[e]);
         }
         if constexpr (W) {
@@ -886,9 +911,13 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
      const long unit = (long)w.b * units_b + w.g * a.nch + w.ch, slot = unit + blockIdx.x;
      for (int n = w.t1 - w.t0; n > 0; --n) {
       warp_wait(&sh.f_full[sb], ph, abort, a.status);
+      if (sh.any_fa[sb]) {
+#pragma unroll
+        for (int r = 0; r < C::kRowsT; r += 2)
+          o[r / 2] = mul2(o[r / 2], *reinterpret_cast<const uint64_t*>(&sh.fa[sb][rb + r]));
+      }
       warp_wait(&sh.o_full[sb], ph, abort, a.status);
       tc::fence_after_sync();
-      const uint64_t c28 = pack2(1.f / 28.f, 1.f / 28.f);
 #pragma unroll
       for (int r0 = 0; r0 < C::kRowsT; r0 += 16) {
         constexpr int kH = C::kRowsT < 16 ? C::kRowsT : 16, q = C::q;
@@ -907,9 +936,9 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
               x2 = __uint_as_float(c[0][x + q + 8]), y2 = __uint_as_float(c[0][x + q + 9]);
             }
           }
-          const float4 f = sh.acc[sb][(rb + r0 + r) / 2];
-          o[(r0 + r) / 2] = fma2(o[(r0 + r) / 2], pack2(f.x, f.y),
-                                 mul2(fma2(pack2(x2, y2), c28, pack2(x1, y1)), pack2(f.z, f.w)));
+          const float4 f = sh.fb[sb][(rb + r0 + r) / 2];
+          uint64_t& y = o[(r0 + r) / 2];
+          y = fma2(pack2(x2, y2), pack2(f.z, f.w), fma2(pack2(x1, y1), pack2(f.x, f.y), y));
         }
       }
       tc::fence_before_sync();
@@ -1136,8 +1165,9 @@ cudaError_t launch_rows(const CUtensorMap& mk, const CUtensorMap& mv, C8AttendAr
   const int rows = a.n_new * (a.Hq / a.G);
   const long items = (long)a.batch * a.G * rows;
   if (items > 0x7FFFFFF0L) return cudaErrorInvalidConfiguration;
-  // eight warps a row while that is a wave of CTAs (a long sequence's rows have many pieces), else one
-  if (items <= 148 * 8)
+  // eight warps a row where a unit has four pieces or more (1M tokens, 4 groups: 8 us instead of 15), else
+  // one (128 units of 2 pieces: 6 us instead of 9)
+  if ((long)a.batch * a.G * rw.nch * 4 <= kGridMax)
     e = launch_behind(cache8_join_kernel<D, NR, kJoinWarps>, (unsigned)items, kJoinWarps * 32, 0, s, true, a);
   else
     e = launch_behind(cache8_join_kernel<D, NR, 1>, (unsigned)((items + kJoinWarps - 1) / kJoinWarps), kJoinWarps * 32, 0,
