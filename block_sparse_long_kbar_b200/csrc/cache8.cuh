@@ -67,6 +67,24 @@ struct C8EvictArgs {
 size_t cache8_keep_bytes(int batch, int G, int T);
 cudaError_t launch_cache8_evict(const C8EvictArgs& a, cudaStream_t s);
 
+// Launch whose start overlaps the end of the kernel before it on the stream (after which it waits
+// where it needs that kernel's results) or, with ahead false, an ordinary one.
+template <class... P, class... A>
+inline cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s, bool ahead,
+                          A... args) {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &at;
+  cfg.numAttrs = ahead ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ---- device helpers ----------------------------------------------------------------------------
 // Exponent of the scale from the bits of the largest finite |x| (an fp32): amax = m 2^E with m in
 // [1, 2) and 448 = 1.75 2^8, so e = E - 8, plus one when m > 1.75, within [-126, 119]. Zeros and fp32

@@ -1086,24 +1086,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache8_join_kernel(C8AttendAr
   if (lane == 0 && a.w_out) a.lse[item] = den == 0.f ? 0.f : m + log2f(den);
 }
 
-// Launch whose start overlaps the end of the kernel before it on the stream (after which it waits
-// where it needs that kernel's results) or, with ahead false, an ordinary one.
-template <class... P, class... A>
-cudaError_t launch_behind(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t s, bool ahead,
-                          A... args) {
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cfg.attrs = &at;
-  cfg.numAttrs = ahead ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);

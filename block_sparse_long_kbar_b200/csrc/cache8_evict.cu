@@ -29,7 +29,8 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* buf, uint32
   }
   if (lane == 31) buf[warp] = y;
   __syncthreads();
-  uint32_t v = buf[lane], z = v;
+  const uint32_t v = lane < (int)(blockDim.x >> 5) ? buf[lane] : 0u;
+  uint32_t z = v;
 #pragma unroll
   for (int h = 1; h < 32; h <<= 1) {
     const uint32_t q = __shfl_up_sync(0xFFFFFFFFu, z, h);
@@ -100,9 +101,10 @@ struct Part {
         eq += key[s][x] == thr ? 1u : 0u;
       }
   }
-  // ng heavier ones and ne equals precede these vectors; both go on behind them
-  __device__ __forceinline__ void emit(int base, uint32_t thr, uint32_t ties, uint32_t& ng, uint32_t& ne,
-                                       int32_t* kept) const {
+  // ng0 heavier ones and ne0 equals precede these vectors
+  __device__ __forceinline__ void emit(int base, uint32_t thr, uint32_t ties, uint32_t ng0, uint32_t ne0, int32_t* kept,
+                                       uint32_t* ng_out = nullptr, uint32_t* ne_out = nullptr) const {
+    uint32_t ng = ng0, ne = ne0;
     const int lane = threadIdx.x & 31;
     const uint32_t below = (1u << lane) - 1u;
 #pragma unroll
@@ -128,19 +130,31 @@ struct Part {
       ng += ag;
       ne += ae;
     }
+    if (ng_out) {
+      *ng_out = ng;
+      *ne_out = ne;
+    }
   }
 };
 
-// Thread t of 1024 holds the counts n0, n1 of bins 2047 - 2 t and 2046 - 2 t: extends the prefix by the
-// bin of the need-th heaviest, and counts need from the top of that bin.
-__device__ __forceinline__ void find_bin(uint32_t n0, uint32_t n1, int pass, uint32_t& prefix, uint32_t& need,
+// Thread t of 2048 / BINS holds the counts n[] of bins 2047 - BINS t and below: extends the prefix by
+// the bin of the need-th heaviest, and counts need from the top of that bin.
+template <int BINS>
+__device__ __forceinline__ void find_bin(const uint32_t (&n)[BINS], int pass, uint32_t& prefix, uint32_t& need,
                                          uint32_t* buf, uint32_t* found) {
-  uint32_t all;
-  const uint32_t before = block_scan(n0 + n1, buf, &all);
-  if (before < need && need <= before + n0 + n1) {
-    const bool second = need > before + n0;
-    found[0] = 2047u - 2u * threadIdx.x - (second ? 1u : 0u);
-    found[1] = need - before - (second ? n0 : 0u);
+  uint32_t sum = 0u, all;
+#pragma unroll
+  for (int i = 0; i < BINS; ++i) sum += n[i];
+  uint32_t before = block_scan(sum, buf, &all);
+  if (before < need && need <= before + sum) {
+#pragma unroll
+    for (int i = 0; i < BINS; ++i) {
+      if (before < need && need <= before + n[i]) {
+        found[0] = 2047u - BINS * threadIdx.x - i;
+        found[1] = need - before;
+      }
+      before += n[i];
+    }
   }
   __syncthreads();
   prefix |= found[0] << (pass == 0 ? 21 : pass == 1 ? 10 : 0);
@@ -175,6 +189,7 @@ __global__ void __launch_bounds__(kSelThr) cache8_keep_kernel(C8EvictArgs a) {
   const cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
   const int unit = blockIdx.x / ctas, tid = threadIdx.x, lane = tid & 31;
+  grid_dependents();
   const int L = c8_len(a.lens, unit / a.G, a.T, a.status);
   if (keep_simple(a, unit, L, rank * kSelThr + tid, ctas * kSelThr)) return;
   Part<VEC> part;
@@ -201,13 +216,13 @@ __global__ void __launch_bounds__(kSelThr) cache8_keep_kernel(C8EvictArgs a) {
   for (int pass = 0; pass < 3; ++pass) {
     pass_over([&](int) { part.count(hist[pass], pass, prefix); });
     cluster.sync();
-    uint32_t n0 = 0u, n1 = 0u;
+    uint32_t bins[2] = {0u, 0u};
     for (int r = 0; r < ctas; ++r) {
       const uint2 h = *cluster.map_shared_rank(reinterpret_cast<uint2*>(&hist[pass][2046 - 2 * tid]), r);
-      n0 += h.y;
-      n1 += h.x;
+      bins[0] += h.y;
+      bins[1] += h.x;
     }
-    find_bin(n0, n1, pass, prefix, need, buf, found);
+    find_bin(bins, pass, prefix, need, buf, found);
   }
   // heavier ones and equals in this warp, this CTA's warps before it, the CTAs before this one
   uint32_t gt = 0u, eq = 0u;
@@ -229,41 +244,49 @@ __global__ void __launch_bounds__(kSelThr) cache8_keep_kernel(C8EvictArgs a) {
     ne += x[1];
   }
   int32_t* kept = a.kept + (long)unit * a.keep;
-  pass_over([&](int base) { part.emit(base, prefix, need, ng, ne, kept); });
+  pass_over([&](int base) { part.emit(base, prefix, need, ng, ne, kept, &ng, &ne); });
   cluster.sync();  // no CTA leaves while another reads its shared memory
 }
 
 // The same selection for few (sequence, group)s of very many weights, which need the whole GPU: a part
-// of 16384 weights per CTA, and a launch per pass (STEP 0 to 2: histograms, added up in global memory;
-// 3: counts of every part; 4: positions). The weights come from L2 after the first.
+// of 8192 weights per CTA, and a launch per pass (STEP 0 to 2: histograms, added up in global memory;
+// 3: counts of every part; 4: positions). The weights come from L2 after the first pass, and are read
+// while the launch before ends.
 // Global memory, per unit: 3 histograms, (prefix, need) after each, (heavier, equal) of every part.
+constexpr int kGridThr = 512;
 template <int STEP>
-__global__ void __launch_bounds__(kSelThr) cache8_keep_grid_kernel(C8EvictArgs a) {
+__global__ void __launch_bounds__(kGridThr) cache8_keep_grid_kernel(C8EvictArgs a) {
   __shared__ alignas(16) uint32_t hist[STEP < 3 ? 2048 : 2];
   __shared__ uint32_t buf[32], found[2];
   const int unit = blockIdx.y, rank = blockIdx.x, ctas = gridDim.x, tid = threadIdx.x, lane = tid & 31;
+  grid_dependents();
   const int L = c8_len(a.lens, unit / a.G, a.T, a.status);
   if (STEP == 0) {
-    if (keep_simple(a, unit, L, rank * kSelThr + tid, ctas * kSelThr)) return;
+    grid_wait();
+    if (keep_simple(a, unit, L, rank * kGridThr + tid, ctas * kGridThr)) return;
   } else if (L <= a.keep || a.keep == a.recent) {
+    grid_wait();  // (no kernel ends before the one it was started behind)
     return;
   }
   uint32_t* g = a.grid_ws + (long)unit * keep_grid_words(ctas);
   uint32_t* state = g + 3 * 2048;  // [3][2]
   uint2* counts = reinterpret_cast<uint2*>(state + 8);
   Part<4> part;
-  part.set(a, unit, L - a.recent, ctas, rank, 32);
+  part.set(a, unit, L - a.recent, ctas, rank, kGridThr / 32);
   part.fetch(part.v0);
   uint32_t prefix = 0u, need = (uint32_t)(a.keep - a.recent);
   if (STEP < 3)
-    for (int i = tid; i < 2048; i += kSelThr) hist[i] = 0u;
+    for (int i = tid; i < 2048; i += kGridThr) hist[i] = 0u;
+  part.keys(part.v0);
+  if (STEP > 0) grid_wait();
   if (STEP > 1) {
     prefix = state[2 * (min(STEP, 4) - 2)];
     need = state[2 * (min(STEP, 4) - 2) + 1];
   }
   if (STEP > 0 && STEP < 4) {
-    const uint2 h = *reinterpret_cast<const uint2*>(g + (STEP - 1) * 2048 + 2046 - 2 * tid);
-    find_bin(h.y, h.x, STEP - 1, prefix, need, buf, found);
+    const uint4 h = *reinterpret_cast<const uint4*>(g + (STEP - 1) * 2048 + 2044 - 4 * tid);
+    const uint32_t bins[4] = {h.w, h.z, h.y, h.x};
+    find_bin(bins, STEP - 1, prefix, need, buf, found);
     if (rank == 0 && tid == 0) {
       state[2 * (STEP - 1)] = prefix;
       state[2 * (STEP - 1) + 1] = need;
@@ -271,11 +294,10 @@ __global__ void __launch_bounds__(kSelThr) cache8_keep_grid_kernel(C8EvictArgs a
   } else {
     __syncthreads();
   }
-  part.keys(part.v0);
   if constexpr (STEP < 3) {
     part.count(hist, STEP, prefix);
     __syncthreads();
-    for (int i = tid; i < 2048; i += kSelThr)
+    for (int i = tid; i < 2048; i += kGridThr)
       if (hist[i]) atomicAdd(g + STEP * 2048 + i, hist[i]);
   } else {
     uint32_t gt = 0u, eq = 0u, all_gt, all_eq;
@@ -289,16 +311,14 @@ __global__ void __launch_bounds__(kSelThr) cache8_keep_grid_kernel(C8EvictArgs a
       ng = __shfl_sync(0xFFFFFFFFu, ng, 0);
       ne = __shfl_sync(0xFFFFFFFFu, ne, 0);
       uint32_t bg = 0u, be = 0u, before_g, before_e;
-      for (int r = tid; r < rank; r += kSelThr) {
+      for (int r = tid; r < rank; r += kGridThr) {
         const uint2 x = counts[r];
         bg += x.x;
         be += x.y;
       }
       block_scan(bg, buf, &before_g);
       block_scan(be, buf, &before_e);
-      ng += before_g;
-      ne += before_e;
-      part.emit(part.v0, prefix, need, ng, ne, a.kept + (long)unit * a.keep);
+      part.emit(part.v0, prefix, need, ng + before_g, ne + before_e, a.kept + (long)unit * a.keep);
     }
   }
 }
@@ -325,98 +345,117 @@ __device__ __forceinline__ uint32_t amax16(const uint4& x, float scale) {
 // kept row is read and written once.
 constexpr int kLoop = 8;
 template <int D, int BLK>
-__global__ void __launch_bounds__(kThr) cache8_move_kernel(C8EvictArgs a, int loop) {
+__global__ void __launch_bounds__(kThr, BLK * D == 128 * 128 ? 4 : 0) cache8_move_kernel(C8EvictArgs a, int loop) {
   constexpr int kTpr = D / 16, kRows = kThr / kTpr;
   constexpr int kItems = kRows > BLK ? kRows / BLK : 1;
   constexpr int kPass = BLK > kRows ? BLK / kRows : 1;
-  __shared__ uint32_t amax[kLoop][kItems][2];
+  constexpr int kSide = kPass == 1 ? 2 : 1;
+  __shared__ uint32_t amax[kLoop + 1][kItems][2];
   const int tid = threadIdx.x, b = blockIdx.y;
+  grid_dependents();
   const int m = min(c8_len(a.lens, b, a.T, a.status), a.keep);
   const int first = (int)blockIdx.x * loop * kItems;
+  for (int i = tid; i < (kLoop + 1) * kItems * 2; i += kThr) (&amax[0][0][0])[i] = 0u;
+  grid_wait();
   if (first / a.G * BLK >= m) return;
-  for (int i = tid; i < kLoop * kItems * 2; i += kThr) (&amax[0][0][0])[i] = 0u;
   __syncthreads();
   const int sub = kItems > 1 ? (tid / kTpr) / BLK : 0;
   const int row0 = kItems > 1 ? (tid / kTpr) % BLK : tid / kTpr;
   const int col = (tid % kTpr) * 16;
   const int nblk = (a.T + BLK - 1) / BLK, nblk_out = (a.T_out + BLK - 1) / BLK;
-  // One step ahead: the rows' positions; with one or two rows per thread also the rows themselves.
-  constexpr bool kAhead = kPass == 2;
+  // kSide items side by side, so that every thread has several rows under way, and their positions one
+  // step ahead
   struct Item {
     int j, g, u[kPass];
     uint4 xk[kPass], xv[kPass];
     int ek[kPass], ev[kPass];
   };
-  auto positions = [&](Item& x) {
+  auto positions = [&](Item& x, bool there) {
 #pragma unroll
     for (int p = 0; p < kPass; ++p) {
       const int i = x.j * BLK + row0 + p * kRows;
-      x.u[p] = i < m ? __ldg(a.kept + (long)(b * a.G + x.g) * a.keep + i) : -1;
+      // (a plain load: written by the kernel before, whose end is waited for in this one)
+      x.u[p] = there && i < m ? a.kept[(long)(b * a.G + x.g) * a.keep + i] : -1;
     }
   };
-  auto fetch = [&](Item& x) {
+  auto step = [&](Item& x) {
+    for (x.g += kItems * kSide; x.g >= a.G; x.g -= a.G) ++x.j;
+  };
+  Item x[kSide], y[kSide];
 #pragma unroll
-    for (int p = 0; p < kPass; ++p) {
-      x.xk[p] = x.xv[p] = make_uint4(0, 0, 0, 0);
-      x.ek[p] = x.ev[p] = -126;
-      if (x.u[p] >= 0) {
-        const long src = (long)((b * a.T + x.u[p]) * a.G + x.g) * D + col;
-        const long si = (long)(b * nblk + x.u[p] / BLK) * a.G + x.g;
-        x.xk[p] = __ldg(reinterpret_cast<const uint4*>(a.src.k8 + src));
-        x.xv[p] = __ldg(reinterpret_cast<const uint4*>(a.src.v8 + src));
-        x.ek[p] = c8_scale_exponent(__ldg(a.src.ks + si));
-        x.ev[p] = c8_scale_exponent(__ldg(a.src.vs + si));
+  for (int q = 0; q < kSide; ++q) {
+    x[q].j = (first + sub + q * kItems) / a.G;
+    x[q].g = (first + sub + q * kItems) % a.G;
+    positions(x[q], q < loop);
+  }
+  for (int it = 0; it < loop; it += kSide) {
+#pragma unroll
+    for (int q = 0; q < kSide; ++q) {
+      Item& z = x[q];
+#pragma unroll
+      for (int p = 0; p < kPass; ++p) {
+        z.xk[p] = z.xv[p] = make_uint4(0, 0, 0, 0);
+        z.ek[p] = z.ev[p] = -126;
+        if (z.u[p] >= 0) {
+          const long src = (long)((b * a.T + z.u[p]) * a.G + z.g) * D + col;
+          const long si = (long)(b * nblk + z.u[p] / BLK) * a.G + z.g;
+          z.xk[p] = __ldg(reinterpret_cast<const uint4*>(a.src.k8 + src));
+          z.xv[p] = __ldg(reinterpret_cast<const uint4*>(a.src.v8 + src));
+          z.ek[p] = c8_scale_exponent(__ldg(a.src.ks + si));
+          z.ev[p] = c8_scale_exponent(__ldg(a.src.vs + si));
+        }
       }
+      y[q].j = z.j;
+      y[q].g = z.g;
+      step(y[q]);
+      positions(y[q], it + kSide + q < loop);
     }
-  };
-  auto next = [&](Item& y, const Item& x) {
-    y.j = x.j;
-    for (y.g = x.g + kItems; y.g >= a.G; y.g -= a.G) ++y.j;
-  };
-  Item x, y;
-  x.j = (first + sub) / a.G;
-  x.g = (first + sub) % a.G;
-  positions(x);
-  if (kAhead) fetch(x);
-  for (int it = 0; it < loop; ++it) {
-    next(y, x);
-    if (it + 1 < loop) positions(y);
-    if (!kAhead) fetch(x);
-    const int i0 = x.j * BLK + row0;
     if (col == 0) {
 #pragma unroll
-      for (int p = 0; p < kPass; ++p)
-        if (x.u[p] >= 0)
-          a.w_out[(long)(b * a.G + x.g) * a.T_out + i0 + p * kRows] = __ldg(a.weight + (long)(b * a.G + x.g) * a.T + x.u[p]);
-    }
-    uint32_t mk = 0, mv = 0;
+      for (int q = 0; q < kSide; ++q)
 #pragma unroll
-    for (int p = 0; p < kPass; ++p) {
-      mk = max(mk, amax16(x.xk[p], c8_pow2(x.ek[p])));
-      mv = max(mv, amax16(x.xv[p], c8_pow2(x.ev[p])));
+        for (int p = 0; p < kPass; ++p)
+          if (x[q].u[p] >= 0)
+            a.w_out[(long)(b * a.G + x[q].g) * a.T_out + x[q].j * BLK + row0 + p * kRows] =
+                __ldg(a.weight + (long)(b * a.G + x[q].g) * a.T + x[q].u[p]);
     }
-    mk = __reduce_max_sync(0xFFFFFFFFu, mk);
-    mv = __reduce_max_sync(0xFFFFFFFFu, mv);
-    if ((tid & 31) == 0) {
-      atomicMax(&amax[it][sub][0], mk);
-      atomicMax(&amax[it][sub][1], mv);
+#pragma unroll
+    for (int q = 0; q < kSide; ++q) {
+      uint32_t mk = 0, mv = 0;
+#pragma unroll
+      for (int p = 0; p < kPass; ++p) {
+        mk = max(mk, amax16(x[q].xk[p], c8_pow2(x[q].ek[p])));
+        mv = max(mv, amax16(x[q].xv[p], c8_pow2(x[q].ev[p])));
+      }
+      mk = __reduce_max_sync(0xFFFFFFFFu, mk);
+      mv = __reduce_max_sync(0xFFFFFFFFu, mv);
+      if ((tid & 31) == 0) {
+        atomicMax(&amax[it + q][sub][0], mk);
+        atomicMax(&amax[it + q][sub][1], mv);
+      }
     }
-    if (kAhead && it + 1 < loop) fetch(y);
     __syncthreads();
-    const int nk = c8_exponent(amax[it][sub][0]), nv = c8_exponent(amax[it][sub][1]);
 #pragma unroll
-    for (int p = 0; p < kPass; ++p) {
-      if (x.u[p] < 0) break;
-      const long dst = (long)((b * a.T_out + i0 + p * kRows) * a.G + x.g) * D + col;
-      *reinterpret_cast<uint4*>(a.dst.k8 + dst) = c8_rescale16(x.xk[p], x.ek[p] - nk);
-      *reinterpret_cast<uint4*>(a.dst.v8 + dst) = c8_rescale16(x.xv[p], x.ev[p] - nv);
+    for (int q = 0; q < kSide; ++q) {
+      const Item& z = x[q];
+      const int nk = c8_exponent(amax[it + q][sub][0]), nv = c8_exponent(amax[it + q][sub][1]);
+#pragma unroll
+      for (int p = 0; p < kPass; ++p) {
+        if (z.u[p] < 0) break;
+        const long dst = (long)((b * a.T_out + z.j * BLK + row0 + p * kRows) * a.G + z.g) * D + col;
+        *reinterpret_cast<uint4*>(a.dst.k8 + dst) = c8_rescale16(z.xk[p], z.ek[p] - nk);
+        *reinterpret_cast<uint4*>(a.dst.v8 + dst) = c8_rescale16(z.xv[p], z.ev[p] - nv);
+      }
+      if (row0 == 0 && col == 0 && z.u[0] >= 0) {
+        const long so = (long)(b * nblk_out + z.j) * a.G + z.g;
+        a.dst.ks[so] = c8_pow2(nk);
+        a.dst.vs[so] = c8_pow2(nv);
+      }
+      x[q].j = y[q].j;
+      x[q].g = y[q].g;
+#pragma unroll
+      for (int p = 0; p < kPass; ++p) x[q].u[p] = y[q].u[p];
     }
-    if (row0 == 0 && col == 0 && x.u[0] >= 0) {
-      const long so = (long)(b * nblk_out + x.j) * a.G + x.g;
-      a.dst.ks[so] = c8_pow2(nk);
-      a.dst.vs[so] = c8_pow2(nv);
-    }
-    x = y;
   }
 }
 
@@ -428,9 +467,8 @@ cudaError_t launch_move(const C8EvictArgs& a, cudaStream_t s) {
   const long items = (long)((most + BLK - 1) / BLK) * a.G;  // of a sequence; T * G is below 2^31
   const long groups = (items + kItems - 1) / kItems, full = groups * a.batch / (148 * 6 * 4);
   const int loop = (int)(full < 1 ? 1 : full > kLoop ? kLoop : full);
-  cache8_move_kernel<D, BLK><<<dim3((unsigned)((groups + loop - 1) / loop), (unsigned)a.batch), kThr, 0, s>>>(
-      a, loop);
-  return cudaGetLastError();
+  return launch_behind(cache8_move_kernel<D, BLK>, dim3((unsigned)((groups + loop - 1) / loop), (unsigned)a.batch), kThr,
+                       0, s, true, a, loop);
 }
 template <int D>
 cudaError_t launch_d(const C8EvictArgs& a, cudaStream_t s) {
@@ -480,7 +518,7 @@ cudaError_t launch_keep(const C8EvictArgs& a, int ctas, cudaStream_t s) {
 // Where 8 do not hold them: launches over the whole GPU if clusters of 16 would leave SMs without a CTA
 // (1M weights, 4 groups: 76 us with 4 clusters of 16), else those.
 bool keep_on_grid(long units, int T) { return !keep_fits(T, 4, 8) && units * 16 <= 148; }
-int keep_grid_ctas(int T) { return (int)(((long)T + 6 + 4 * kSelPart - 1) / (4 * kSelPart)); }
+int keep_grid_ctas(int T) { return (int)(((long)T + 6 + 16 * kGridThr - 1) / (16 * kGridThr)); }
 cudaError_t launch_keep_any(const C8EvictArgs& a, cudaStream_t s) {
   const long units = (long)a.batch * a.G;
   if (keep_on_grid(units, a.T)) {
@@ -488,12 +526,12 @@ cudaError_t launch_keep_any(const C8EvictArgs& a, cudaStream_t s) {
     cudaError_t e = cudaMemsetAsync(a.grid_ws, 0, (size_t)units * keep_grid_words(ctas) * 4, s);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)ctas, (unsigned)units);
-    cache8_keep_grid_kernel<0><<<grid, kSelThr, 0, s>>>(a);
-    cache8_keep_grid_kernel<1><<<grid, kSelThr, 0, s>>>(a);
-    cache8_keep_grid_kernel<2><<<grid, kSelThr, 0, s>>>(a);
-    cache8_keep_grid_kernel<3><<<grid, kSelThr, 0, s>>>(a);
-    cache8_keep_grid_kernel<4><<<grid, kSelThr, 0, s>>>(a);
-    return cudaGetLastError();
+    cache8_keep_grid_kernel<0><<<grid, kGridThr, 0, s>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_behind(cache8_keep_grid_kernel<1>, grid, kGridThr, 0, s, true, a)) != cudaSuccess) return e;
+    if ((e = launch_behind(cache8_keep_grid_kernel<2>, grid, kGridThr, 0, s, true, a)) != cudaSuccess) return e;
+    if ((e = launch_behind(cache8_keep_grid_kernel<3>, grid, kGridThr, 0, s, true, a)) != cudaSuccess) return e;
+    return launch_behind(cache8_keep_grid_kernel<4>, grid, kGridThr, 0, s, true, a);
   }
   int c = 1;
   while (c < 8 && (!keep_fits(a.T, 4, c) || (units * c * 2 <= 148 && a.T >= c * 2 * 2048))) c *= 2;
