@@ -87,7 +87,8 @@ struct Shared {
 
 // The tiles of one CTA in order, a piece of a unit at a time: tiles [t0, t1) of unit ((sequence b,
 // group g), chunk ch of its rows). A loop over a piece's tiles has nothing else to keep track of: with
-// four roles on every scheduler, instruction fetch is what short loops are for.
+// four roles on every scheduler, instruction fetch is what short loops are for. The weights' pass goes
+// from the last tile to the first, for K tiles that the first pass has left in L2.
 struct Walk {
   int b, g, ch, L, ntiles, t0, t1, left;  // left: tiles of this and later pieces
   int piece, k;                           // pieces and tiles of this CTA before
@@ -97,37 +98,44 @@ __device__ __forceinline__ int len_of(const C8AttendArgs& a, int b) {
   const int n = __ldg(a.lens + b);
   return n >= 0 && n <= a.T ? n : 0;
 }
+// off: the CTA's first tile (back: its last one) among the sequence's
+template <bool BACK>
 __device__ __forceinline__ void walk_begin(Walk& w, const C8AttendArgs& a, int b, int off, int left) {
   w.b = b;
   w.L = len_of(a, b);
   w.ntiles = tiles_of(w.L);
-  const int gu = off / w.ntiles;
+  const int gu = off / w.ntiles, tile = off - gu * w.ntiles;
   w.g = gu / a.nch;
-  w.ch = gu % a.nch;
-  w.t0 = off % w.ntiles;
+  w.ch = gu - w.g * a.nch;
   w.left = left;
-  w.t1 = min(w.ntiles, w.t0 + left);
+  w.t0 = BACK ? max(0, tile + 1 - left) : tile;
+  w.t1 = BACK ? tile + 1 : min(w.ntiles, tile + left);
   w.piece = w.k = 0;
 }
+template <bool BACK>
 __device__ __forceinline__ void walk_next(Walk& w, const C8AttendArgs& a) {
   w.left -= w.t1 - w.t0;
   w.k += w.t1 - w.t0;
   ++w.piece;
   if (w.left == 0) return;
-  if (++w.ch == a.nch) {
-    w.ch = 0;
-    if (++w.g == a.G) {
-      w.g = 0;
+  w.ch += BACK ? -1 : 1;
+  if (w.ch < 0 || w.ch == a.nch) {
+    w.ch = BACK ? a.nch - 1 : 0;
+    w.g += BACK ? -1 : 1;
+    if (w.g < 0 || w.g == a.G) {
+      w.g = BACK ? a.G - 1 : 0;
       do {
-        ++w.b;
+        w.b += BACK ? -1 : 1;
         w.L = len_of(a, w.b);
       } while (w.L == 0);
       w.ntiles = tiles_of(w.L);
     }
   }
-  w.t0 = 0;
-  w.t1 = min(w.ntiles, w.left);
+  w.t0 = BACK ? max(0, w.ntiles - w.left) : 0;
+  w.t1 = BACK ? w.ntiles : min(w.ntiles, w.left);
 }
+template <bool BACK>
+__device__ __forceinline__ int walk_tile(const Walk& w, int x) { return BACK ? w.t1 - 1 - x : w.t0 + x; }
 
 // Per launch: partial sums of every piece, and the CTAs that hold a unit's first and last tile.
 template <int D, int NR>
@@ -206,6 +214,19 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
   return r;
+}
+__device__ __forceinline__ uint64_t evict_first_policy() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void tma_load_3d_once(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z,
+                                                 uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%3, %4, "
+      "%5}], [%2], %6;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "l"(policy)
+      : "memory");
 }
 // True in one lane of the warp, the same one each time.
 __device__ __forceinline__ bool elect_one() {
@@ -295,86 +316,69 @@ __device__ __forceinline__ int v_chunk(int row, int c) {
   return D == 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3);
 }
 
-// Rows r_begin, r_begin + r_step, .. of a unit's q as two E4M3 terms, and what else a row needs; a warp
-// per row, eight rows' loads at a time.
+// A unit's rows of q as two E4M3 terms, and what else a row needs: warp `first` of `warps`, D / 16 lanes
+// to a row, 16 dims a lane. (A loop of little code: it runs once per unit, mostly from a cold
+// instruction cache; with eight rows unrolled it took 9 us.)
 template <int D, int NR, bool W>
-__device__ __forceinline__ void split_q(const C8AttendArgs& a, const Walk& w, Shared<NR>& sh, uint8_t* sQ, int r_begin,
-                                        int r_step, int lane) {
+__device__ __forceinline__ void split_q(const C8AttendArgs& a, const Walk& w, Shared<NR>& sh, uint8_t* sQ, int first,
+                                        int warps, int lane) {
   using C = Cfg<D, NR, W>;
-  constexpr int kE = D / 32;
+  constexpr int kLanes = D / 16, kRows = 32 / kLanes;
   const int R = a.Hq / a.G, rows = a.n_new * R;
   const int pb = w.piece & 1, r0 = w.ch * a.chunk_rows, real = min(a.chunk_rows, rows - r0);
-  uint8_t* dst = sQ + pb * C::kQ;
-  for (int r = r_begin + lane * r_step; r < NR; r += 32 * r_step) {
-    sh.lim[pb][r] = r < real ? w.L - a.n_new + (r0 + r) / R : -1;
-    // (no row: 2^-inf)
-    if (W) sh.lse[pb][r] = r < real ? a.lse[((long)w.b * a.G + w.g) * rows + r0 + r] : INFINITY;
-  }
-  for (int r8 = r_begin; r8 < NR; r8 += 8 * r_step) {
-    uint32_t x[8][kE / 2];
+  const int chunk = lane % kLanes;
+  uint8_t* dst = sQ + pb * C::kQ + chunk * 128;
+#pragma unroll 1
+  for (int r = first * kRows + lane / kLanes; r < NR; r += warps * kRows) {
+    const int gr = r0 + r, i = gr / R;
+    uint4 x[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+    float lse = INFINITY;  // no row: 2^-inf
+    if (r < real) {
+      const uint4* src = reinterpret_cast<const uint4*>(
+          a.q + (((long)w.b * a.n_new + i) * a.Hq + (long)w.g * R + gr - i * R) * D + chunk * 16);
+      x[0] = __ldg(src);
+      x[1] = __ldg(src + 1);
+      if (W) lse = a.lse[((long)w.b * a.G + w.g) * rows + gr];
+    }
+    const uint32_t y[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+    uint32_t amax = 0u;
 #pragma unroll
-    for (int y = 0; y < 8; ++y) {
-      const int r = r8 + y * r_step;
-#pragma unroll
-      for (int e = 0; e < kE / 2; ++e) x[y][e] = 0u;
-      if (r < real) {
-        const int gr = r0 + r;
-        const long src = (((long)w.b * a.n_new + gr / R) * a.Hq + (long)w.g * R + gr % R) * D + lane * kE;
-        if constexpr (kE == 4) {
-          const uint2 v = __ldg(reinterpret_cast<const uint2*>(a.q + src));
-          x[y][0] = v.x;
-          x[y][1] = v.y;
-        } else {
-          x[y][0] = __ldg(reinterpret_cast<const uint32_t*>(a.q + src));
-        }
-      }
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t lo = y[e] & 0x7FFFu, hi = (y[e] >> 16) & 0x7FFFu;
+      amax = max(amax, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
     }
 #pragma unroll
-    for (int y = 0; y < 8; ++y) {
-      const int r = r8 + y * r_step;
-      if (r < NR) {
-      uint32_t amax = 0u;
+    for (int h = 1; h < kLanes; h <<= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, h));
+    const int ex = c8_exponent(amax << 16);
+    const float inv = c8_pow2(-ex);
+    uint32_t c1[4], c2[4];
 #pragma unroll
-      for (int e = 0; e < kE / 2; ++e) {
-        const uint32_t lo = x[y][e] & 0x7FFFu, hi = (x[y][e] >> 16) & 0x7FFFu;
-        amax = max(amax, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
-      }
-      amax = __reduce_max_sync(0xFFFFFFFFu, amax);
-      const int ex = c8_exponent(amax << 16);
-      const float inv = c8_pow2(-ex);
-      uint32_t c1 = 0u, c2 = 0u;
-#pragma unroll
-      for (int e = 0; e < kE / 2; ++e) {
-        const float y0 = bf16_lo(x[y][e]) * inv, y1 = bf16_hi(x[y][e]) * inv;
-        uint32_t t1 = c8_encode2(y0, y1);
-        const float2 f = c8_decode2(t1);
-        const uint32_t t2 = c8_encode2((y0 - f.x) * 16.f, (y1 - f.y) * 16.f);
-        // an infinity becomes NaN, as which it would end in the scores
-        if ((x[y][e] & 0x7F80u) == 0x7F80u) t1 |= 0x7Fu;
-        if ((x[y][e] & 0x7F800000u) == 0x7F800000u) t1 |= 0x7F00u;
-        c1 |= t1 << (16 * e);
-        c2 |= t2 << (16 * e);
-      }
-      // columns 8 j + 2 i + x of S^T: row i q + (j / 2) 2 + x, term j % 2
-      const int at = (lane * kE / 16) * 128 + lane * kE % 16;
-      const int jj = r % C::q, n1 = 16 * (jj >> 1) + 2 * (r / C::q) + (jj & 1), n2 = n1 + 8;
-      uint8_t* p1 = dst + (n1 >> 3) * (D * 8) + (n1 & 7) * 16 + at;
-      uint8_t* p2 = dst + (n2 >> 3) * (D * 8) + (n2 & 7) * 16 + at;
-      if constexpr (kE == 4) {
-        *reinterpret_cast<uint32_t*>(p1) = c1;
-        *reinterpret_cast<uint32_t*>(p2) = c2;
-      } else {
-        *reinterpret_cast<uint16_t*>(p1) = (uint16_t)c1;
-        *reinterpret_cast<uint16_t*>(p2) = (uint16_t)c2;
-      }
-      if (lane == 0) sh.fac[pb][r] = c8_pow2(ex) * (kLog2e / sqrtf((float)D));
-      }
+    for (int e = 0; e < 8; ++e) {
+      const float y0 = bf16_lo(y[e]) * inv, y1 = bf16_hi(y[e]) * inv;
+      uint32_t t1 = c8_encode2(y0, y1);
+      const float2 f = c8_decode2(t1);
+      const uint32_t t2 = c8_encode2((y0 - f.x) * 16.f, (y1 - f.y) * 16.f);
+      // an infinity becomes NaN, as which it would end in the scores
+      if ((y[e] & 0x7F80u) == 0x7F80u) t1 |= 0x7Fu;
+      if ((y[e] & 0x7F800000u) == 0x7F800000u) t1 |= 0x7F00u;
+      c1[e / 2] = e & 1 ? c1[e / 2] | (t1 << 16) : t1;
+      c2[e / 2] = e & 1 ? c2[e / 2] | (t2 << 16) : t2;
+    }
+    // columns 8 j + 2 i + x of S^T: row i q + (j / 2) 2 + x, term j % 2
+    const int jj = r % C::q, n1 = 16 * (jj >> 1) + 2 * (r / C::q) + (jj & 1), n2 = n1 + 8;
+    *reinterpret_cast<uint4*>(dst + (n1 >> 3) * (D * 8) + (n1 & 7) * 16) = make_uint4(c1[0], c1[1], c1[2], c1[3]);
+    *reinterpret_cast<uint4*>(dst + (n2 >> 3) * (D * 8) + (n2 & 7) * 16) = make_uint4(c2[0], c2[1], c2[2], c2[3]);
+    if (chunk == 0) {
+      sh.fac[pb][r] = c8_pow2(ex) * (kLog2e / sqrtf((float)D));
+      sh.lim[pb][r] = r < real ? w.L - a.n_new + i : -1;
+      if (W) sh.lse[pb][r] = lse;
     }
   }
+  __syncwarp();
   tc::fence_proxy_async();
 }
 
-// One of the warps that split q: rows first, first + kQWarps, .. of the piece w, and of all later ones.
+// One of the kQWarps warps that split q: its rows of the piece w, and of all later ones.
 template <int D, int NR, bool W>
 __device__ __forceinline__ void split_piece(const C8AttendArgs& a, const Walk& w, Shared<NR>& sh, uint8_t* sQ, int first,
                                             volatile int* abort, int lane) {
@@ -386,7 +390,7 @@ __device__ __forceinline__ void split_piece(const C8AttendArgs& a, const Walk& w
 template <int D, int NR, bool W>
 __device__ __forceinline__ void split_all(const C8AttendArgs& a, Walk w, Shared<NR>& sh, uint8_t* sQ, int first,
                                           volatile int* abort, int lane) {
-  for (walk_next(w, a); w.left > 0; walk_next(w, a)) split_piece<D, NR, W>(a, w, sh, sQ, first, abort, lane);
+  for (walk_next<W>(w, a); w.left > 0; walk_next<W>(w, a)) split_piece<D, NR, W>(a, w, sh, sQ, first, abort, lane);
 }
 
 template <int D, int NR, bool W>
@@ -455,11 +459,12 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
   const int each = total / n, odd = total - each * n;
   const int t0 = each * cta + min(cta, odd), t1 = t0 + each + (cta < odd ? 1 : 0);
   if (warp == 1) tc::tmem_alloc(&sh.tmem, C::kTmem);
-  if (upto > t0 && upto - mine <= t0) {
+  const int from = W ? t1 - 1 : t0;
+  if (upto > from && upto - mine <= from) {
     sh.start_b = tid;
-    sh.start_off = t0 - (upto - mine);
+    sh.start_off = from - (upto - mine);
   }
-  for (int b0 = kThreads; seen <= t0; b0 += kThreads) {
+  for (int b0 = kThreads; seen <= from; b0 += kThreads) {
     const int b = b0 + tid, nb = b < a.batch ? tiles_of(len_of(a, b)) * units_b : 0;
     int x = warp_scan(nb, lane);
     __syncthreads();
@@ -470,9 +475,9 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
       if (i < warp) x += sh.wsum[i];
       seen += sh.wsum[i];
     }
-    if (x > t0 && x - nb <= t0) {
+    if (x > from && x - nb <= from) {
       sh.start_b = b;
-      sh.start_off = t0 - (x - nb);
+      sh.start_off = from - (x - nb);
     }
   }
   tc::fence_before_sync();
@@ -482,7 +487,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
   const uint32_t tmem_o = tmem + kGroups * C::N;
   volatile int* abort = &sh.abort_flag;
   Walk w;
-  walk_begin(w, a, sh.start_b, sh.start_off, t1 - t0);
+  walk_begin<W>(w, a, sh.start_b, sh.start_off, t1 - t0);
   const Part<D, NR> part(a.part, (long)a.batch * units_b);
 
   // the first piece's rows of q: all warps but those that have tiles to fetch and to multiply
@@ -506,17 +511,24 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
     int k = 0, st = 0;
     uint32_t ph = 1;
     bool stop = false;
-    for (; w.left > 0 && !stop; walk_next(w, a)) {
+    const uint64_t once = evict_first_policy();  // V where K is read again for the weights
+    for (; w.left > 0 && !stop; walk_next<W>(w, a)) {
       const float* src = scales + ((long)w.b * nblk + j) * a.G + w.g;
       const int z = w.b * a.T;
-      for (int tile = w.t0; tile < w.t1; ++tile, ++k) {
+      for (int x = 0; x < w.t1 - w.t0; ++x, ++k) {
+        const int tile = walk_tile<W>(w, x);
         if (k >= C::kStages) warp_wait(&sh.empty[st], ph, abort, a.status);
         if ((stop = __any_sync(0xFFFFFFFFu, *abort))) break;
         if (lane == 0) {
           uint8_t* dst = sKV + st * C::kStage;
           tc::mbar_arrive_expect_tx(&sh.full[st], C::kStage);
           tc::tma_load_3d(dst, &map_k, &sh.full[st], 0, w.g, z + tile * kTok);
-          if (!W) tc::tma_load_3d(dst + C::kTile, &map_v, &sh.full[st], 0, w.g, z + tile * kTok);
+          if (W) {
+          } else if (a.w_out) {
+            tma_load_3d_once(dst + C::kTile, &map_v, &sh.full[st], 0, w.g, z + tile * kTok, once);
+          } else {
+            tc::tma_load_3d(dst + C::kTile, &map_v, &sh.full[st], 0, w.g, z + tile * kTok);
+          }
         }
         const long blk = (long)tile * per;
         if (mine && blk + j < nblk) cp_async4(&sh.scale[st][lane], src + blk * a.G);
@@ -540,7 +552,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
     const uint64_t dk = tc::smem_desc_kmajor(sKV, D), dq = tc::smem_desc_kmajor_noswz(sQ, 128, D * 8);
     int k = 0, st = 0, sb = 0;
     uint32_t ph = 0, sph = 1;  // phases of the stages and of S^T's buffers
-    for (; w.left > 0; walk_next(w, a)) {
+    for (; w.left > 0; walk_next<W>(w, a)) {
       const int pb = w.piece & 1;
       const uint64_t db = dq + (uint32_t)(pb * (C::kQ >> 4));
       warp_wait(&sh.q_full[pb], (uint32_t)((w.piece >> 1) & 1), abort, a.status);
@@ -622,7 +634,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
       float m_run = kNegMax, l = 0.f;
       int e_run = -126, sb = 0;
       uint32_t ph = 0;
-      for (; w.left > 0; walk_next(w, a)) {
+      for (; w.left > 0; walk_next<W>(w, a)) {
         for (int n = w.t1 - w.t0; n > 0; --n) {
           warp_wait(&sh.p_full[sb], ph, abort, a.status);
           float now = 1.f;
@@ -673,14 +685,15 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
     // tiles k = wg, wg + groups, ..: stage k mod the stages, phase of the buffers kp = k / groups
     int st = wg;
     uint32_t ph = 0, kp = 0;
-    for (; w.left > 0; walk_next(w, a)) {
+    for (; w.left > 0; walk_next<W>(w, a)) {
       const int pb = w.piece & 1;
       warp_wait(&sh.q_full[pb], (uint32_t)((w.piece >> 1) & 1), abort, a.status);
 #pragma unroll
       for (int j = 0; j < q / 2; ++j) fac[j] = pack2(sh.fac[pb][row0 + 2 * j], sh.fac[pb][row0 + 2 * j + 1]);
       const int vis = w.L - a.n_new;  // tokens up to here are visible to every row
       const long wi0 = ((long)w.b * a.G + w.g) * a.T;
-      for (int tile = w.t0 + (wg + kGroups - w.k % kGroups) % kGroups; tile < w.t1; tile += kGroups, ++kp) {
+      for (int x = (wg + kGroups - w.k % kGroups) % kGroups; x < w.t1 - w.t0; x += kGroups, ++kp) {
+        const int tile = walk_tile<W>(w, x);
         const int u0 = tile * kTok + tok;
         const bool edge = (tile + 1) * kTok - 1 > vis;
         const int uw = tile * kTok + q4 * 32 + (lane >> 2) + 8 * i;  // the token whose weight this lane writes
@@ -905,7 +918,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
     int sb = 0;
     uint32_t ph = 0;
     for (Walk ahead = w; w.left > 0; w = ahead) {
-     walk_next(ahead, a);
+     walk_next<W>(ahead, a);
      if (ahead.left > 0) split_piece<D, NR, W>(a, ahead, sh, sQ, q_first, abort, lane);
      const int pb = w.piece & 1;
      const long unit = (long)w.b * units_b + w.g * a.nch + w.ch, slot = unit + blockIdx.x;
