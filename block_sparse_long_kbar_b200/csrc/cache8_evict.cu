@@ -376,6 +376,7 @@ __global__ void __launch_bounds__(kThr, BLK * D == 128 * 128 ? 4 : 0) cache8_mov
       const int i = x.j * BLK + row0 + p * kRows;
       // (a plain load: written by the kernel before, whose end is waited for in this one)
       x.u[p] = there && i < m ? a.kept[(long)(b * a.G + x.g) * a.keep + i] : -1;
+      if (!SGQA_CHECK(x.u[p] < a.T, a.status)) x.u[p] = -1;
     }
   };
   auto step = [&](Item& x) {

@@ -156,6 +156,10 @@ def test_refusals_evict(lib):
     assert evict(lib, v8o=GOOD) == 1
     assert evict(lib, wo=GOOD) == 1
     assert evict(lib, lo=GOOD) == 1
+    assert evict(lib, T_out=1 << 28) == 1
+    assert evict(lib, D(batch=64), T_out=1 << 27) == 2   # 2^34 rows in all
+    long = D(batch=1, T=200000)                          # a selection with histograms in the workspace
+    assert evict(lib, long, ws_bytes=256) == 3 and sg.sgqa_cache8_workspace_size(long, 16, 1) > 256
 
 
 def test_binding_refuses_host_tensors(lib):

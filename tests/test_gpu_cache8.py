@@ -3,12 +3,16 @@
 
 Tolerances. Codes, scales, positions and moved weights are compared exactly. An output element is
 off by at most
-  * the rounding of the probabilities to two E4M3 terms: 2^-4 of each by the first, 2^-4 of the rest by
-    the second, so 2^-8 of p and hence 2^-8 of sum p |v|; below the second term's subnormal step
-    2^-23 of its tile's largest p v-scale, so 128 * 2^-23 = 2^-16 of the largest |v|;
+  * the rounding of the probabilities to two E4M3 terms. Rounding to four significant bits is off by
+    at most 1/17 of a value (half a step of 1/8 at 17/16), so the two by 1/289 of p; the fp16 step
+    before them by 2^-11 of it: together below 2^-8 + 2^-14 of p and hence of sum p |v|. Where the terms
+    are subnormal: the second is 28 times the first's rest and its half step 2^-10, with 448 for the
+    largest p v-scale, so 2^-10 / (28 * 448) = 2^-23.6 of that; over a tile's 128 tokens 2^-16 of the
+    largest |v|;
   * the scores' error: q as two E4M3 terms keeps 2^-22 of its row's largest element and products are
     summed in fp32, so with |q| <= 6 and sum |k| <= 1000 a base-2 exponent is off by less than
-    2^-22 * 6 * 1000 * log2(e) / 8 < 2^-12, and numerator and denominator by 2^-12 each: 2^-11;
+    2^-22 * 6 * 1000 * log2(e) / 8 < 2^-11.9, and by 2^-24 of itself from fp32; numerator and denominator
+    by 0.7 times that each in relative terms: with the 2^-14 above below 2^-11;
   * the output's own rounding, 2^-8 of its value (bf16).
 A received weight is a sum of fp32 probabilities: each off by 2^-11 of itself at most by the same bound,
 and 2^-24 of the total by each fp32 addition (at most 66 of them).
@@ -332,6 +336,97 @@ def test_attend_offsets_beyond_32_bits():
         assert bool(((w[0, h].double() - p).abs() <= 2.0 ** -11 * p + 1e-12).all())
 
 
+def nan_rows(out, want):
+    """Where a plain form gives NaN the kernel does, and nowhere else."""
+    assert torch.equal(torch.isnan(out), torch.isnan(want))
+
+
+@pytest.mark.parametrize("n_new,L", [(64, 130), (64, 64), (40, 300), (64, 257), (17, 9)])
+def test_attend_nan_values_over_two_tiles_of_new_tokens(n_new, L):
+    """NaN V codes among the new tokens: the rows before them are as without, those that see one are NaN in its dim."""
+    gen = torch.Generator().manual_seed(n_new + L)
+    G, d, block = 2, 64, 8
+    c = c8.filled_cache(gen, [L, L], L + 3, G, d, block)
+    q, gate = queries(gen, 2, n_new, G, d)
+    base, _ = check_attend(c8.to_cuda(c), block, [L, L], q, gate, False)
+    want = base.clone()
+    for b, (u, g, x) in enumerate([(L - 1, 0, 3), (max(0, L - n_new // 2), 1, 63)]):
+        c["v8"][b, u, g, x] = 0x7F if b else 0xFF
+        c["v8"][b, u, g, 0] = 0x7F
+        first = max(0, u - (L - n_new))  # the first row that sees token u
+        want[b, first:, g, x] = math.nan
+        want[b, first:, g, 0] = math.nan
+    dm = dims(2, L + 3, G, G, d)
+    ws, out = workspace(dm, block, n_new), torch.zeros_like(q)
+    c = c8.to_cuda(c)
+    sg.sgqa_cache8_attend(dm, block, i32([L, L]), n_new, q, gate, *cache_args(c), out, ws)
+    torch.cuda.synchronize()
+    nan_rows(out, want)
+    assert torch.equal(torch.nan_to_num(out), torch.nan_to_num(want))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_attend_rows_of_nan_and_infinity(d):
+    """A query with a NaN or an infinity gives NaN, its neighbours what they give without it."""
+    gen = torch.Generator().manual_seed(d)
+    lens, G, block = [300, 129], 2, 32
+    c = c8.to_cuda(c8.filled_cache(gen, lens, 300, G, d, block))
+    q, gate = queries(gen, 2, 2, 16, d)
+    base, base_w = check_attend(c, block, lens, q, gate)
+    q[0, 1, 3, 5], q[1, 0, 9, d - 1], q[1, 1, 0, 0] = math.nan, math.inf, -math.inf
+    dm = dims(2, 300, 16, G, d)
+    ws, out, w = workspace(dm, block, 2), torch.zeros_like(q), torch.full((2, G, 300), -7.0, device="cuda")
+    sg.sgqa_cache8_attend(dm, block, i32(lens), 2, q, gate, *cache_args(c), out, ws, weight_out=w)
+    torch.cuda.synchronize()
+    bad = torch.zeros(2, 2, 16, dtype=torch.bool, device="cuda")
+    bad[0, 1, 3] = bad[1, 0, 9] = bad[1, 1, 0] = True
+    assert bool(torch.isnan(out[bad]).all()) and torch.equal(out[~bad], base[~bad])
+    # group 1 of sequence 0 has none of those rows
+    assert torch.equal(w[0, 1], base_w[0, 1]) and bool(torch.isnan(w[0, 0, :300]).all())
+    # row 0 of sequence 1 does not see the last token
+    assert bool(torch.isnan(w[1, 1, :128]).all()) and torch.equal(w[1, 1, 128:], base_w[1, 1, 128:])
+
+
+def test_attend_extreme_scales():
+    """V blocks at both ends of the scales' range, and a token of nearly all weight whose V block is all zero."""
+    gen = torch.Generator().manual_seed(16)
+    L, G, d, block = 400, 1, 128, 16
+    c = c8.filled_cache(gen, [L], L, G, d, block)
+    q, gate = queries(gen, 1, 1, 4, d)
+    for top in (2.0 ** 119, 2.0 ** -100):
+        c["vs"][:] = top
+        c["vs"][0, ::3] = 2.0 ** -126
+        check_attend(c8.to_cuda(c), block, [L], q, gate)
+    k, v = c8.tokens(gen, 1, L, G, d, 0.0), c8.tokens(gen, 1, L, G, d, 0.0)
+    k[0, 0, 0] = (q[0, 0].float().sum(0) * 4).cpu().bfloat16()
+    v[0, :block] = 0.0
+    c = c8.ref_append(c8.empty_cache(1, L, G, d, block, device="cpu"), block, [0], [L], k, v)
+    check_attend(c8.to_cuda(c), block, [L], q, gate)
+
+
+def test_attend_more_rows_than_one_unit_holds_over_many_ctas():
+    gen = torch.Generator().manual_seed(17)
+    lens, G, block = [6000, 0, 3], 1, 64
+    for d, R, n in ((128, 16, 4), (64, 11, 3)):
+        c = c8.to_cuda(c8.filled_cache(gen, lens, 6001, G, d, block))
+        q, gate = queries(gen, 3, n, G * R, d)
+        check_attend(c, block, lens, q, gate)
+
+
+def test_calls_refuse_tensors_elsewhere():
+    gen = torch.Generator().manual_seed(18)
+    c = c8.to_cuda(c8.filled_cache(gen, [20], 32, 1, 64, 8))
+    dm = dims(1, 32, 1, 1, 64)
+    ws, (q, gate) = workspace(dm, 8), queries(gen, 1, 1, 1, 64)
+    with pytest.raises(ValueError):
+        sg.sgqa_cache8_attend(dm, 8, torch.tensor([20], dtype=torch.int32), 1, q, gate, *cache_args(c), torch.zeros_like(q), ws)
+    with pytest.raises(ValueError):
+        wide = torch.zeros((1, 1, 1, 128), dtype=torch.bfloat16, device="cuda")
+        sg.sgqa_cache8_attend(dm, 8, i32([20]), 1, wide[..., ::2], gate, *cache_args(c), torch.zeros_like(q), ws)
+    with pytest.raises(sg.SgqaError):
+        sg.sgqa_cache8_attend(dm, 8, i32([20]), 1, q, gate, *cache_args(c), torch.zeros_like(q), ws[256:512])
+
+
 # ---- evict -----------------------------------------------------------------------------------------
 def run_evict(cache, block, lens, keep, recent, weight, T_out):
     batch, T, G, d = cache["k8"].shape
@@ -437,6 +532,74 @@ def test_evict_long():
             want = (c8.grid(xb / s[:, None, None]) * s[:, None, None]).view(-1, 64)[:65537]
             assert torch.equal(got[scale][b, :len(s), 0].double(), s)
             assert torch.equal(c8.values(got[codes][b, :65537], got[scale][b], 32)[:, 0], want)
+
+
+def random_codes(gen, batch, T, G, d, block):
+    """A cache of random codes, made on the GPU (the ordinary one's plain form is slow)."""
+    c = {n: torch.randint(0, 0x7F, (batch, T, G, d), generator=gen, dtype=torch.uint8, device="cuda") for n in ("k8", "v8")}
+    c.update({n: torch.exp2(torch.randint(-9, -5, (batch, -(-T // block), G), generator=gen, device="cuda").float())
+              for n in ("ks", "vs")})
+    return c
+
+
+def same_eviction(got, c, w, lens, keep, recent, block):
+    """Positions, weights and values of an eviction, a (sequence, group) at a time."""
+    batch, T, G, d = c["k8"].shape
+    for b, L in enumerate(lens):
+        for g in range(G):
+            rows = c8.ref_kept(w[b, g], L, keep, recent)
+            m = len(rows)
+            assert torch.equal(got["kept"][b, g, :m].long(), rows) and bool((got["kept"][b, g, m:] == -1).all())
+            assert same(got["w"][b, g, :m], w[b, g][rows])
+            for codes, scale in (("k8", "ks"), ("v8", "vs")):
+                x = c8.decode(c[codes][b, rows, g]) * c[scale][b, rows // block, g].double()[:, None]
+                xb = torch.nn.functional.pad(x, (0, 0, 0, -m % block)).view(-1, block, d)
+                s = c8.scale_of(xb.abs().amax(dim=(1, 2)))
+                assert torch.equal(got[scale][b, :len(s), g].double(), s)
+                want = c8.grid(xb / s[:, None, None]).view(-1, d)[:m]
+                assert torch.equal(c8.decode(got[codes][b, :m, g]), want)
+
+
+# one CTA per (sequence, group) with 1, 2 and 4 loads a lane; clusters of 2, 4, 8; of 16; the whole GPU
+@pytest.mark.parametrize("batch,G,T,keep,recent", [
+    (1, 1, 1, 1, 0), (60, 2, 4096, 1000, 3), (80, 1, 8191, 4000, 0), (75, 1, 16380, 8000, 100), (75, 1, 16381, 700, 1),
+    (1, 2, 5003, 1234, 17), (2, 1, 9002, 8999, 2), (1, 1, 20001, 333, 333), (1, 1, 131071, 60000, 5),
+    (5, 2, 140003, 70001, 1000), (3, 1, 131073, 1, 0), (1, 1, 500002, 1000, 0)])
+def test_evict_every_selection(batch, G, T, keep, recent):
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    c = random_codes(gen, batch, T, G, 64, 32)
+    w = torch.exp2(torch.randn((batch, G, T), generator=gen, device="cuda") * 3)
+    w[:, :, 5:T // 2:3] = 0.75  # many equal, of which some stay
+    w[:, :, T // 3:T // 3 + 40] = math.nan
+    lens = [T if b % 3 == 0 else T - (b * 37) % (T // 2 + 1) for b in range(batch)]
+    got, _, status = run_evict(c, 32, lens, keep, recent, w, keep + 5)
+    assert status == 0
+    same_eviction(got, c, w, lens, keep, recent, 32)
+
+
+@pytest.mark.parametrize("T,keep", [(3000, 500), (150000, 9000)])
+def test_a_captured_eviction_serves_every_length(T, keep):
+    gen = torch.Generator(device="cuda").manual_seed(T + 1)
+    c = random_codes(gen, 2, T, 1, 64, 64)
+    w = torch.rand((2, 1, T), generator=gen, device="cuda")
+    dst = c8.empty_cache(2, keep, 1, 64, 64)
+    dst.update(w=torch.zeros((2, 1, keep), device="cuda"), kept=torch.zeros((2, 1, keep), dtype=torch.int32, device="cuda"))
+    dm, lens, lens_out = dims(2, T, 1, 1, 64), i32([0, 0]), i32([0, 0])
+    ws = workspace(dm, 64)
+    call = lambda: sg.sgqa_cache8_evict(dm, 64, lens, keep, 7, keep, w, *cache_args(c), *cache_args(dst), dst["w"], dst["kept"],
+                                        lens_out, ws)
+    call()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        call()
+    for ls in ([T, keep + 1], [keep, 0], [T - 5, T]):
+        lens.copy_(i32(ls))
+        w.copy_(torch.rand(w.shape, generator=gen, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert sg.sgqa_get_device_status(ws) == 0 and lens_out.tolist() == [min(x, keep) for x in ls]
+        same_eviction(dst, c, w, ls, keep, 7, 64)
 
 
 # ---- together, streams, graphs ----------------------------------------------------------------------
