@@ -48,6 +48,7 @@ struct C8AttendArgs {
   int batch, T, Hq, G, d, block, n_new;
   // set by the launch: chunks of rows per (sequence, group), rows of each, log2 of block
   int nch, chunk_rows, block_log2;
+  int main_ctas;  // and, for the join, the CTAs of the launch before
   int* status;
 };
 size_t cache8_part_bytes(int batch, int G, int rows, int d);

@@ -1006,29 +1006,50 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
 
 // Joins the pieces of a unit: PER warps per (sequence, group, row), which take its pieces in turn; a
 // lane per piece for the factors, per D / 32 head dims for the sums. The order is fixed.
-constexpr int kJoinWarps = 8;
+constexpr int kJoinWarps = 8, kJoinLens = 256;  // (with more sequences the first kernel's notes are read)
 template <int D, int NR, int PER>
 __global__ void __launch_bounds__(kJoinWarps * 32) cache8_join_kernel(C8AttendArgs a) {
   constexpr int kV = D / 32;
   __shared__ float s_m[kJoinWarps], s_l[kJoinWarps], s_o[PER > 1 ? kJoinWarps : 1][D];
   __shared__ int s_e[kJoinWarps];
   grid_dependents();
-  grid_wait();
-  if (tc::grid_timed_out(a.status)) return;
   const int R = a.Hq / a.G, rows = a.n_new * R, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int item = (blockIdx.x * kJoinWarps + warp) / PER, part_of = warp % PER;
-  if (item >= a.batch * a.G * rows) return;
+  const int item = min((int)((blockIdx.x * kJoinWarps + warp) / PER), a.batch * a.G * rows - 1), part_of = warp % PER;
   const int gr = item % rows, bg = item / rows, b = bg / a.G, g = bg % a.G;
-  const int r = gr % a.chunk_rows;
-  const long unit = (long)bg * a.nch + gr / a.chunk_rows;
+  const int r = gr % a.chunk_rows, ch = gr / a.chunk_rows;
+  const long unit = (long)bg * a.nch + ch;
   const Part<D, NR> part(a.part, (long)a.batch * a.G * a.nch);
   const long at = (((long)b * a.n_new + gr / R) * a.Hq + (long)g * R + gr % R) * D + lane * kV;
+  // what the call's inputs say, while the kernel before still runs
   uint32_t gate[kV / 2];
 #pragma unroll
   for (int v = 0; v < kV / 2; ++v) gate[v] = __ldg(reinterpret_cast<const uint32_t*>(a.gate + at) + v);
-  const int c0 = part.first[unit], c1 = part.last[unit];  // (read before it is known that there are such)
-  const bool some = len_of(a, b) > a.n_new - 1 - gr / R;
-  const int n = some ? c1 - c0 + 1 : 0;  // pieces; this warp's are part_of, part_of + PER, ..
+  const int L = len_of(a, b);
+  const bool some = L > a.n_new - 1 - gr / R;
+  int c0 = 0, c1 = -1;  // the CTAs whose pieces this unit has
+  if (a.batch <= kJoinLens) {
+    int before = 0, total = 0;
+    for (int x = lane; x < a.batch; x += 32) {
+      const int n = tiles_of(len_of(a, x)) * a.G * a.nch;
+      total += n;
+      if (x < b) before += n;
+    }
+    total = __reduce_add_sync(0xFFFFFFFFu, total);
+    before = __reduce_add_sync(0xFFFFFFFFu, before) + (g * a.nch + ch) * tiles_of(L);
+    const int n = max(1, min(a.main_ctas, total)), each = total / n, odd = total - each * n;
+    auto cta_of = [&](int t) { return t < odd * (each + 1) ? t / (each + 1) : odd + (t - odd * (each + 1)) / max(1, each); };
+    if (some) {
+      c0 = cta_of(before);
+      c1 = cta_of(before + tiles_of(L) - 1);
+    }
+  }
+  grid_wait();
+  if (tc::grid_timed_out(a.status) || (blockIdx.x * kJoinWarps + warp) / PER > item) return;
+  if (some && a.batch > kJoinLens) {
+    c0 = part.first[unit];
+    c1 = part.last[unit];
+  }
+  const int n = c1 - c0 + 1;  // pieces; this warp's are part_of, part_of + PER, ..
   float m = kNegMax, den = 0.f, o[kV];
   int e = -126;
 #pragma unroll
@@ -1131,6 +1152,11 @@ bool make_map(CUtensorMap* map, const void* base, long tokens, int G, int d) {
              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+unsigned main_grid(const C8AttendArgs& a) {
+  const long tiles = (long)a.batch * a.G * a.nch * ((a.T + kTok - 1) / kTok);
+  return (unsigned)(tiles < kGridMax ? tiles : kGridMax);
+}
+
 template <int D, int NR, bool W>
 cudaError_t launch_main(const CUtensorMap& mk, const CUtensorMap& mv, C8AttendArgs a, int nch, int chunk_rows,
                         cudaStream_t s) {
@@ -1141,8 +1167,7 @@ cudaError_t launch_main(const CUtensorMap& mk, const CUtensorMap& mv, C8AttendAr
   a.nch = nch;
   a.chunk_rows = chunk_rows;
   a.block_log2 = a.block == 8 ? 3 : a.block == 16 ? 4 : a.block == 32 ? 5 : a.block == 64 ? 6 : 7;
-  const long tiles = (long)a.batch * a.G * nch * ((a.T + kTok - 1) / kTok);
-  const unsigned grid = (unsigned)(tiles < kGridMax ? tiles : kGridMax);
+  const unsigned grid = main_grid(a);
   return launch_behind(cache8_attend_kernel<D, NR, W>, grid, C::kThreads, kSmem, s, W, mk, mv, a);
 }
 
@@ -1161,6 +1186,7 @@ cudaError_t launch_rows(const CUtensorMap& mk, const CUtensorMap& mv, C8AttendAr
   if (e != cudaSuccess) return e;
   a.nch = rw.nch;
   a.chunk_rows = rw.chunk_rows;
+  a.main_ctas = (int)main_grid(a);
   const int rows = a.n_new * (a.Hq / a.G);
   const long items = (long)a.batch * a.G * rows;
   if (items > 0x7FFFFFF0L) return cudaErrorInvalidConfiguration;

@@ -249,13 +249,13 @@ __global__ void __launch_bounds__(kSelThr) cache8_keep_kernel(C8EvictArgs a) {
 }
 
 // The same selection for few (sequence, group)s of very many weights, which need the whole GPU: a part
-// of 8192 weights per CTA, and a launch per pass (STEP 0 to 2: histograms, added up in global memory;
+// of 16384 weights per CTA, and a launch per pass (STEP 0 to 2: histograms, added up in global memory;
 // 3: counts of every part; 4: positions). The weights come from L2 after the first pass, and are read
 // while the launch before ends.
 // Global memory, per unit: 3 histograms, (prefix, need) after each, (heavier, equal) of every part.
-constexpr int kGridThr = 512;
+constexpr int kGridThr = 512, kGridVec = 8;
 template <int STEP>
-__global__ void __launch_bounds__(kGridThr) cache8_keep_grid_kernel(C8EvictArgs a) {
+__global__ void __launch_bounds__(kGridThr, 2) cache8_keep_grid_kernel(C8EvictArgs a) {
   __shared__ alignas(16) uint32_t hist[STEP < 3 ? 2048 : 2];
   __shared__ uint32_t buf[32], found[2];
   const int unit = blockIdx.y, rank = blockIdx.x, ctas = gridDim.x, tid = threadIdx.x, lane = tid & 31;
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kGridThr) cache8_keep_grid_kernel(C8EvictArgs 
   uint32_t* g = a.grid_ws + (long)unit * keep_grid_words(ctas);
   uint32_t* state = g + 3 * 2048;  // [3][2]
   uint2* counts = reinterpret_cast<uint2*>(state + 8);
-  Part<4> part;
+  Part<kGridVec> part;
   part.set(a, unit, L - a.recent, ctas, rank, kGridThr / 32);
   part.fetch(part.v0);
   uint32_t prefix = 0u, need = (uint32_t)(a.keep - a.recent);
@@ -519,7 +519,7 @@ cudaError_t launch_keep(const C8EvictArgs& a, int ctas, cudaStream_t s) {
 // Where 8 do not hold them: launches over the whole GPU if clusters of 16 would leave SMs without a CTA
 // (1M weights, 4 groups: 76 us with 4 clusters of 16), else those.
 bool keep_on_grid(long units, int T) { return !keep_fits(T, 4, 8) && units * 16 <= 148; }
-int keep_grid_ctas(int T) { return (int)(((long)T + 6 + 16 * kGridThr - 1) / (16 * kGridThr)); }
+int keep_grid_ctas(int T) { return (int)(((long)T + 6 + 4 * kGridVec * kGridThr - 1) / (4 * kGridVec * kGridThr)); }
 cudaError_t launch_keep_any(const C8EvictArgs& a, cudaStream_t s) {
   const long units = (long)a.batch * a.G;
   if (keep_on_grid(units, a.T)) {
