@@ -15,8 +15,13 @@ constexpr int kSelPart = 4 * kSelThr;  // weights of a CTA per 16-byte load of i
 // Words of global memory that the selection over the whole GPU has per unit.
 __device__ __host__ constexpr long keep_grid_words(int ctas) { return 3 * 2048 + 8 + 2L * ((ctas + 1) & ~1); }
 
-// Order-preserving key of a weight; NaN ranks as -infinity. No weight's key is 0.
-__device__ __forceinline__ uint32_t weight_key(float w) { return score_key(w != w ? -INFINITY : w); }
+// Order-preserving key of a weight: -0 as +0, NaN as -infinity. No weight's key is 0.
+__device__ __forceinline__ uint32_t weight_key(float w) {
+  const float x = w + 0.f;
+  const int u = __float_as_int(x);
+  const uint32_t k = (uint32_t)(u ^ ((u >> 31) | (int)0x80000000));
+  return x == x ? k : 0x007FFFFFu;
+}
 
 // Sum of x over the block's threads before this one; *all: over all.
 __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* buf, uint32_t* all) {
@@ -48,38 +53,50 @@ template <int VEC>
 struct Part {
   const float* w;
   int off, N, v0, v1;
+  int w0, w1;  // vectors all of whose weights compete: [w0, w1)
   uint32_t key[VEC][4];
   float4 ahead[VEC];
   __device__ __forceinline__ void set(const C8EvictArgs& a, int unit, int n, int ctas, int rank, int warps) {
-    const long w0 = (long)unit * a.T;
-    off = (int)(w0 & 3);
-    w = a.weight + (w0 - off);
+    const long at = (long)unit * a.T;
+    off = (int)(at & 3);
+    w = a.weight + (at - off);
     N = n;
     const int nv = (N + off + 3) / 4, per_cta = (nv + ctas - 1) / ctas, per_warp = (per_cta + warps - 1) / warps;
     v0 = rank * per_cta + (int)(threadIdx.x >> 5) * per_warp;
     v1 = min(min(nv, (rank + 1) * per_cta), v0 + per_warp);
+    w0 = off ? 1 : 0;
+    w1 = min(v1, (N + off) >> 2);
   }
-  __device__ __forceinline__ bool whole(int v) const { return v < v1 && 4 * v - off >= 0 && 4 * v - off + 3 < N; }
   __device__ __forceinline__ void fetch(int base) {
+    const int v = base + (int)(threadIdx.x & 31);
+    const float4* p = reinterpret_cast<const float4*>(w) + v;
 #pragma unroll
-    for (int s = 0; s < VEC; ++s) {
-      const int v = base + s * 32 + (int)(threadIdx.x & 31);
-      if (whole(v)) ahead[s] = __ldg(reinterpret_cast<const float4*>(w) + v);
-    }
+    for (int s = 0; s < VEC; ++s)
+      if (v + s * 32 >= w0 && v + s * 32 < w1) ahead[s] = __ldg(p + s * 32);
   }
   __device__ __forceinline__ void keys(int base) {  // 0 where there is no weight
+    const int v = base + (int)(threadIdx.x & 31);
 #pragma unroll
     for (int s = 0; s < VEC; ++s) {
-      const int v = base + s * 32 + (int)(threadIdx.x & 31), e = 4 * v - off;
-      if (whole(v)) {
-        key[s][0] = weight_key(ahead[s].x);
-        key[s][1] = weight_key(ahead[s].y);
-        key[s][2] = weight_key(ahead[s].z);
-        key[s][3] = weight_key(ahead[s].w);
-      } else {
+      const bool whole = v + s * 32 >= w0 && v + s * 32 < w1;
+      key[s][0] = whole ? weight_key(ahead[s].x) : 0u;
+      key[s][1] = whole ? weight_key(ahead[s].y) : 0u;
+      key[s][2] = whole ? weight_key(ahead[s].z) : 0u;
+      key[s][3] = whole ? weight_key(ahead[s].w) : 0u;
+    }
+    if (base < w0 || w1 < min(v1, base + VEC * 32)) {  // the unit's first or last vector, in part
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-          key[s][x] = v < v1 && e + x >= 0 && e + x < N ? weight_key(__ldg(w + 4L * v + x)) : 0u;
+      for (int s = 0; s < VEC; ++s) {
+        const int y = v + s * 32;
+        if (y < v1 && (y < w0 || y >= w1))
+          for (int x = 0; x < 4; ++x) {
+            const int e = 4 * y - off + x;
+            const uint32_t k = e >= 0 && e < N ? weight_key(__ldg(w + 4L * y + x)) : 0u;
+            if (x == 0) key[s][0] = k;
+            else if (x == 1) key[s][1] = k;
+            else if (x == 2) key[s][2] = k;
+            else key[s][3] = k;
+          }
       }
     }
   }
@@ -101,34 +118,45 @@ struct Part {
         eq += key[s][x] == thr ? 1u : 0u;
       }
   }
-  // ng0 heavier ones and ne0 equals precede these vectors
+  // ng0 heavier ones and ne0 equals precede these vectors. A lane's counts in two vectors, heavier and
+  // equal, are four bytes of a word (a warp has at most 128 of each), so that one scan over the lanes
+  // serves both.
   __device__ __forceinline__ void emit(int base, uint32_t thr, uint32_t ties, uint32_t ng0, uint32_t ne0, int32_t* kept,
                                        uint32_t* ng_out = nullptr, uint32_t* ne_out = nullptr) const {
-    uint32_t ng = ng0, ne = ne0;
     const int lane = threadIdx.x & 31;
-    const uint32_t below = (1u << lane) - 1u;
+    uint32_t ng = ng0, ne = ne0;
 #pragma unroll
-    for (int s = 0; s < VEC; ++s) {
-      uint32_t lg = 0u, le = 0u, ag = 0u, ae = 0u;  // in the lanes below, in all lanes
+    for (int s0 = 0; s0 < VEC; s0 += 2) {
+      uint32_t own = 0u;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const uint32_t bg = __ballot_sync(0xFFFFFFFFu, key[s][x] > thr);
-        const uint32_t be = __ballot_sync(0xFFFFFFFFu, key[s][x] == thr);
-        lg += __popc(bg & below);
-        le += __popc(be & below);
-        ag += __popc(bg);
-        ae += __popc(be);
+      for (int s = s0; s < min(VEC, s0 + 2); ++s)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint32_t one = 1u << (16 * (s - s0));
+          own += key[s][x] > thr ? one : 0u;
+          own += key[s][x] == thr ? one << 8 : 0u;
+        }
+      uint32_t upto = own;
+#pragma unroll
+      for (int h = 1; h < 32; h <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, upto, h);
+        if (lane >= h) upto += y;
       }
-      uint32_t pg = ng + lg, pe = ne + le;
+      const uint32_t all = __shfl_sync(0xFFFFFFFFu, upto, 31), before = upto - own;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const bool is_gt = key[s][x] > thr, is_eq = key[s][x] == thr;
-        if (is_gt || (is_eq && pe < ties)) kept[pg + min(pe, ties)] = 4 * (base + s * 32 + lane) - off + x;
-        pg += is_gt ? 1u : 0u;
-        pe += is_eq ? 1u : 0u;
+      for (int s = s0; s < min(VEC, s0 + 2); ++s) {
+        const int sh = 16 * (s - s0);
+        uint32_t pg = ng + (before >> sh & 255u), pe = ne + (before >> (sh + 8) & 255u);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const bool is_gt = key[s][x] > thr, is_eq = key[s][x] == thr;
+          if (is_gt || (is_eq && pe < ties)) kept[pg + min(pe, ties)] = 4 * (base + s * 32 + lane) - off + x;
+          pg += is_gt ? 1u : 0u;
+          pe += is_eq ? 1u : 0u;
+        }
+        ng += all >> sh & 255u;
+        ne += all >> (sh + 8) & 255u;
       }
-      ng += ag;
-      ne += ae;
     }
     if (ng_out) {
       *ng_out = ng;
