@@ -10,11 +10,12 @@
 
 using namespace sgqa;
 
+int sgqa::g_test_stall_cta = -1;
+
 namespace {
 
 constexpr int kSelChunkT = 32768;  // query rows per selection chunk when sel stays in ws
 constexpr size_t kSelBitsBudget = 256ull << 20;  // bitmaps of the taken candidates (K2 -> block lists)
-int g_test_stall_cta = -1;         // sgqa_test_stall_decode_cta (failure-detection tests only)
 
 struct PrefillWs {
   int* status;

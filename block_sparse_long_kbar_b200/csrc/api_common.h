@@ -8,6 +8,8 @@
 
 namespace sgqa {
 
+extern int g_test_stall_cta;  // sgqa_test_stall_decode_cta (failure-detection tests only)
+
 inline bool aligned16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 inline int check_dims(const sgqa_dims* d) {

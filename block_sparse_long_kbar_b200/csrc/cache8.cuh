@@ -46,6 +46,7 @@ struct C8AttendArgs {
   float* lse;         // [batch, G, n_new * R]: log2 of each row's softmax sum
   float* part;
   int batch, T, Hq, G, d, block, n_new;
+  int stall_cta;  // failure-detection test hook: this CTA issues no loads (-1: none)
   // set by the launch: chunks of rows per (sequence, group), rows of each, log2 of block
   int nch, chunk_rows, block_log2;
   int main_ctas;  // and, for the join, the CTAs of the launch before

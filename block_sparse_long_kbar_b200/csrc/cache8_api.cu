@@ -95,7 +95,7 @@ int sgqa_cache8_attend(const sgqa_dims* dims, int block, const int32_t* lens, in
   a.lens = lens; a.q = q; a.gate = gate; a.c = cache_of(k8, k_scale, v8, v_scale); a.out = out;
   a.w_in = weight_in; a.w_out = weight_out; a.lse = w.lse; a.part = w.part;
   a.batch = dims->batch; a.T = dims->T; a.Hq = dims->Hq; a.G = dims->G; a.d = dims->d; a.block = block;
-  a.n_new = n_new; a.status = w.status;
+  a.n_new = n_new; a.status = w.status; a.stall_cta = g_test_stall_cta;
   return cuda_status(launch_cache8_attend(a, static_cast<cudaStream_t>(stream)));
 }
 

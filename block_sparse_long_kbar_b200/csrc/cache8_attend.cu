@@ -70,7 +70,7 @@ struct Shared {
   float scale[8][32];                      // per stage: K scales of the tile's blocks, then V scales
   uint32_t tmem;
   volatile int abort_flag;
-  int start_b, start_off;
+  int start_b, start_off, stopped;
   int wsum[32], wmore[32];
   int nan_any[2];
   int nan_at[2][128];                      // per head dim: first token not visible to all rows whose V is NaN there
@@ -424,6 +424,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
   } else if (tid == 32) {
     tc::prefetch_tensormap(&map_k);
     if (!W) tc::prefetch_tensormap(&map_v);
+  } else if (tid == 64) {
+    sh.stopped = tc::grid_timed_out(a.status);
   }
   if (tid < 18) tc::fence_mbar_init();
   if (tid < 256) sh.nan_at[tid >> 7][tid & 127] = kNever;
@@ -448,7 +450,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
   total += seen;
   // (every CTA below n has a tile: the CTAs between a unit's first and last have all written)
   const int n = min((int)gridDim.x, total), cta = (int)blockIdx.x;
-  if (cta >= n) {
+  if (cta >= n || sh.stopped) {
     if (W) grid_wait();  // (no kernel ends before the one it was started behind)
     return;
   }
@@ -508,7 +510,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
     const bool mine = j < per && !(W && part_v);
     int issued = 0, st = me;
     uint32_t ph = 1;
-    bool stop = false;
+    bool stop = !W && (int)blockIdx.x == a.stall_cta;
     const uint64_t once = evict_first_policy();  // V where K is read again for the weights
     for (; w.left > 0 && !stop; walk_next<W>(w, a)) {
       const float* src = scales + ((long)w.b * nblk + j) * a.G + w.g;
@@ -684,6 +686,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
     uint64_t fac[q / 2];
 #pragma unroll
     for (int j = 0; j < q / 2; ++j) fac[j] = 0ull;
+    const bool stopped = W && tc::grid_timed_out(a.status);  // the rows' sums were not written
     // tiles k = wg, wg + groups, ..: stage k mod the stages, phase of the buffers kp = k / groups
     int st = wg;
     uint32_t ph = 0, kp = 0;
@@ -797,7 +800,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
           const float h0 = (up2 ? add[2] : add[0]) + __shfl_xor_sync(0xFFFFFFFFu, g0, 2);
           const float h1 = (up2 ? add[3] : add[1]) + __shfl_xor_sync(0xFFFFFFFFu, g1, 2);
           const float tot = (up1 ? h1 : h0) + __shfl_xor_sync(0xFFFFFFFFu, up1 ? h0 : h1, 1);
-          if (uw < w.L) a.w_out[wi] = sum + tot;
+          if (uw < w.L && !stopped) a.w_out[wi] = sum + tot;
         } else {
           // maxima of the tile; NaN counts for none (it reaches the sums by itself)
           float mx[q];

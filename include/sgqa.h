@@ -266,6 +266,10 @@ int sgqa_cache8_append(const sgqa_dims* dims, int block, const int32_t* lens, co
  *   (u < lens[b] - n_new ? weight_in[b,g,u] : 0) + sum over i and the heads of g of its probability,
  * the attention weight it has received so far, when weight_in [batch, G, T] is what the step before
  * wrote (NULL: nothing yet; it may be weight_out itself).
+ * A query with a NaN or an infinity gives NaN, itself and (visible tokens') weights; a NaN in V only the
+ * dims and rows that see it. K and V are read from the codes as they are: q and the probabilities go to
+ * the tensor cores as two E4M3 terms each (q exact but for elements below 2^-14 of their row's largest,
+ * probabilities to 2^-8), scores, maxima, denominators and received weights are fp32.
  * Requires n_new * Hq/G <= 64 (else SGQA_ERR_UNSUPPORTED). */
 int sgqa_cache8_attend(const sgqa_dims* dims, int block, const int32_t* lens, int n_new, const uint16_t* q,
                        const uint16_t* gate, const uint8_t* k8, const float* k_scale, const uint8_t* v8,
@@ -280,7 +284,7 @@ int sgqa_cache8_attend(const sgqa_dims* dims, int block, const int32_t* lens, in
  * take the scale of their new block; a row whose scale does not change keeps its bits. Writes
  *   kept [batch, G, keep] int32, the positions that stay, ascending, then -1;
  *   lens_out [batch] int32 = min(lens[b], keep);  weight_out [batch, G, T_out], the weights that stay.
- * No output may overlap an input. */
+ * No output may overlap an input. batch * T_out * G < 2^31 (else SGQA_ERR_UNSUPPORTED). */
 int sgqa_cache8_evict(const sgqa_dims* dims, int block, const int32_t* lens, int keep, int recent, int T_out,
                       const float* weight, const uint8_t* k8, const float* k_scale, const uint8_t* v8,
                       const float* v_scale, uint8_t* k8_out, float* k_scale_out, uint8_t* v8_out,
@@ -288,7 +292,8 @@ int sgqa_cache8_evict(const sgqa_dims* dims, int block, const int32_t* lens, int
                       size_t ws_bytes, void* stream);
 
 /* Failure-detection test hook (host-side setting, not for production use). While cta >= 0, the
- * decode attention CTA with that grid index in later sgqa_decode / sgqa_decode_fp8 calls issues
+ * decode attention CTA with that grid index in later sgqa_decode / sgqa_decode_fp8 calls (and the
+ * attention CTA in sgqa_cache8_attend) issues
  * no loads, so its tensor-core issuer's wait for the first tile is never satisfied: the wait
  * runs out after its bound (2 s), the kernel records SGQA_ERR_TIMEOUT in the status word and
  * returns with nothing in flight, and every other CTA and later kernel that polls that status

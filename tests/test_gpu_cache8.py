@@ -427,6 +427,36 @@ def test_calls_refuse_tensors_elsewhere():
         sg.sgqa_cache8_attend(dm, 8, i32([20]), 1, q, gate, *cache_args(c), torch.zeros_like(q), ws[256:512])
 
 
+def test_a_wait_that_runs_out_ends_the_call():
+    """One CTA issues no loads (the hook's flag that nothing sets): the call ends with the status recorded,
+    the next one stops at once and writes nothing, and after a reset all is as before."""
+    gen = torch.Generator().manual_seed(19)
+    lens, G, d, block = [900, 500], 2, 128, 32
+    c = c8.to_cuda(c8.filled_cache(gen, lens, 900, G, d, block))
+    q, gate = queries(gen, 2, 4, 16, d)
+    base, base_w = check_attend(c, block, lens, q, gate)
+    dm = dims(2, 900, 16, G, d)
+    ws = workspace(dm, block, 4)
+    out, w = torch.full_like(q, math.nan), torch.full((2, G, 900), -7.0, device="cuda")
+    call = lambda: sg.sgqa_cache8_attend(dm, block, i32(lens), 4, q, gate, *cache_args(c), out, ws, weight_out=w)
+    sg.sgqa_test_stall_decode_cta(1)
+    try:
+        call()
+        torch.cuda.synchronize()
+    finally:
+        sg.sgqa_test_stall_decode_cta(-1)
+    assert sg.sgqa_get_device_status(ws) == 5
+    for _ in range(2):
+        call()
+        torch.cuda.synchronize()
+        assert sg.sgqa_get_device_status(ws) == 5
+        assert bool(torch.isnan(out).all()) and bool((w == -7).all())
+    sg.sgqa_reset_device_status(ws)
+    call()
+    torch.cuda.synchronize()
+    assert sg.sgqa_get_device_status(ws) == 0 and torch.equal(out, base) and torch.equal(w, base_w)
+
+
 # ---- evict -----------------------------------------------------------------------------------------
 def run_evict(cache, block, lens, keep, recent, weight, T_out):
     batch, T, G, d = cache["k8"].shape
