@@ -117,33 +117,44 @@ def _ptr(t, name):
     return t.data_ptr()
 
 
-def _here(ws):
-    """The device of ws, which has to be the current one."""
+def _current_device():
+    """Index of the current device (bound to torch's own function on first use)."""
+    global _current_device
     import torch
-    dev = ws.get_device()
-    if dev < 0:
-        raise ValueError("ws must be a CUDA tensor")
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"ws is on device {dev}, not on the current one")
-    return dev
+    torch.cuda.current_device()  # (initialises CUDA)
+    _current_device = torch._C._cuda_getDevice
+    return _current_device()
 
 
-def _at(t, name, dev):
-    """Address of a contiguous tensor on device dev (None stays None)."""
-    if t is None:
-        return None
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be a CUDA tensor on the device of ws")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+def _addresses(names, tensors):
+    """Addresses of contiguous tensors (None stays None), all on the current device; the last is ws."""
+    dev, out = tensors[-1].get_device(), []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+        elif t.get_device() != dev or dev < 0:
+            raise ValueError(f"{names.split()[len(out)]} must be a CUDA tensor on the device of ws")
+        elif not t.is_contiguous():
+            raise ValueError(f"{names.split()[len(out)]} must be contiguous")
+        else:
+            out.append(t.data_ptr())
+    if dev != _current_device():
+        raise ValueError(f"the tensors are on device {dev}, not on the current one")
+    return out
+
+
+def _current_stream(device):
+    """Raw handle of a device's current stream, without building a Stream object, which takes some 3 us: as
+    long as a small call's kernels (bound to torch's own function on first use)."""
+    global _current_stream
+    import torch
+    _current_stream = torch._C._cuda_getCurrentRawStream
+    return _current_stream(device)
 
 
 def _stream(stream):
-    import torch
     if stream is None:
-        # (without building a Stream object, which takes some 3 us: as long as a small call's kernels)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _current_stream(_current_device())
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -307,35 +318,31 @@ def sgqa_cache8_workspace_size(dims: sgqa_dims, block: int, n_new: int) -> int:
 
 def sgqa_cache8_append(dims, block, lens, n_t, k_new, v_new, k8, k_scale, v8, v_scale, ws, counts=None, stream=None):
     """Store the first counts[b] (default: all n_t) tokens of k_new, v_new behind the lens[b] cached ones."""
-    dev = _here(ws)
+    p = _addresses("lens counts k_new v_new k8 k_scale v8 v_scale ws",
+                   (lens, counts, k_new, v_new, k8, k_scale, v8, v_scale, ws))
     _check("sgqa_cache8_append", load_library().sgqa_cache8_append(
-        ctypes.byref(dims), int(block), _at(lens, "lens", dev), _at(counts, "counts", dev), int(n_t), _at(k_new, "k_new", dev),
-        _at(v_new, "v_new", dev), _at(k8, "k8", dev), _at(k_scale, "k_scale", dev), _at(v8, "v8", dev), _at(v_scale, "v_scale", dev),
-        _at(ws, "ws", dev), ws.numel(), _stream(stream)))
+        ctypes.byref(dims), int(block), p[0], p[1], int(n_t), *p[2:], ws.numel(), _stream(stream)))
 
 
 def sgqa_cache8_attend(dims, block, lens, n_new, q, gate, k8, k_scale, v8, v_scale, out, ws, weight_in=None,
                        weight_out=None, stream=None):
     """Dense gated attention of the last n_new of lens[b] tokens over the block-scaled 8-bit cache; with
     weight_out, also the attention weight that every token has received (on top of weight_in)."""
-    dev = _here(ws)
+    p = _addresses("lens q gate k8 k_scale v8 v_scale out weight_in weight_out ws",
+                   (lens, q, gate, k8, k_scale, v8, v_scale, out, weight_in, weight_out, ws))
     _check("sgqa_cache8_attend", load_library().sgqa_cache8_attend(
-        ctypes.byref(dims), int(block), _at(lens, "lens", dev), int(n_new), _at(q, "q", dev), _at(gate, "gate", dev),
-        _at(k8, "k8", dev), _at(k_scale, "k_scale", dev), _at(v8, "v8", dev), _at(v_scale, "v_scale", dev), _at(out, "out", dev),
-        _at(weight_in, "weight_in", dev), _at(weight_out, "weight_out", dev), _at(ws, "ws", dev), ws.numel(), _stream(stream)))
+        ctypes.byref(dims), int(block), p[0], int(n_new), *p[1:], ws.numel(), _stream(stream)))
 
 
 def sgqa_cache8_evict(dims, block, lens, keep, recent, T_out, weight, k8, k_scale, v8, v_scale, k8_out, k_scale_out,
                       v8_out, v_scale_out, weight_out, kept, lens_out, ws, stream=None):
     """Move the `recent` last and the heaviest other tokens, `keep` in all per (sequence, group), to
     another cache of capacity T_out."""
-    dev = _here(ws)
+    p = _addresses("lens weight k8 k_scale v8 v_scale k8_out k_scale_out v8_out v_scale_out weight_out kept lens_out ws",
+                   (lens, weight, k8, k_scale, v8, v_scale, k8_out, k_scale_out, v8_out, v_scale_out, weight_out, kept,
+                    lens_out, ws))
     _check("sgqa_cache8_evict", load_library().sgqa_cache8_evict(
-        ctypes.byref(dims), int(block), _at(lens, "lens", dev), int(keep), int(recent), int(T_out),
-        _at(weight, "weight", dev), _at(k8, "k8", dev), _at(k_scale, "k_scale", dev), _at(v8, "v8", dev), _at(v_scale, "v_scale", dev),
-        _at(k8_out, "k8_out", dev), _at(k_scale_out, "k_scale_out", dev), _at(v8_out, "v8_out", dev),
-        _at(v_scale_out, "v_scale_out", dev), _at(weight_out, "weight_out", dev), _at(kept, "kept", dev),
-        _at(lens_out, "lens_out", dev), _at(ws, "ws", dev), ws.numel(), _stream(stream)))
+        ctypes.byref(dims), int(block), p[0], int(keep), int(recent), int(T_out), *p[1:], ws.numel(), _stream(stream)))
 
 
 def sgqa_test_stall_decode_cta(cta: int):
