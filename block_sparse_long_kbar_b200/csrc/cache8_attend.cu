@@ -8,7 +8,7 @@
 // or head dims), and the few query rows of a (sequence, group) are the narrow one:
 //   S^T[128 tokens x 2 NR] = K_tile . [q1; q2]^T       q = (q1 + q2 / 16) 2^e, both E4M3
 //   O^T[d x 2 NR]          = V_tile^T . [P1 | P2]      p t = (P1 + P2 / 28) 2^E / 448, both E4M3
-// Two E4M3 terms hold q exactly down to 2^-22 of its row's largest element and p t to 2^-8 of itself
+// Two E4M3 terms hold q exactly down to 2^-14 of its row's largest element and p t to 2^-8 of itself
 // or 2^-23 of the tile's largest. P is relative to its own tile's maxima (of z per row, of t over the
 // tile), so O^T starts anew in every tile and is added up in registers in fp32: a token that takes
 // nearly all attention costs the far ones none of their digits. The denominator and the maxima are
@@ -18,13 +18,27 @@
 // contiguous piece per CTA (one CTA per SM), so that ragged lengths, one long sequence and many
 // short ones all balance; the lengths are read on the device. A unit's pieces leave partial sums,
 // which a second kernel joins in the order of the tiles.
-// Roles: warp 0 issues TMA loads, warp 1 the MMAs of S^T, warp 2 those of O^T, warp 3
-// splits the rows of q, warps 4-7 and 8-11 take tiles in turn from S^T to P, warps 12-15 (a thread per
-// head dim) add O^T up. Waits are bounded as everywhere (tc_common.cuh).
+// Roles: warp 0 issues TMA loads, warp 1 the MMAs of S^T, warp 2 those of O^T, warp 3 keeps the rows'
+// running maxima and sums, then come two or three groups of four warps that take tiles in turn from
+// S^T to P, and four warps (a thread per head dim) that add O^T up and split the next unit's rows of
+// q. Waits are bounded as everywhere (tc_common.cuh): after one has run out nobody waits any more, and
+// the roles run through their tiles to the end.
 // S^T is read in the 16x256b shape: a lane holds NR / 4 rows of 4 tokens (q's rows are placed so that
 // both terms of a row and pairs of rows land in one lane), so that row factors take NR / 4 registers,
 // maxima and sums over tokens start inside the thread, and products run on packed pairs.
-// The received weights need each row's final sum: a further pass over K recomputes the scores.
+// The received weights need each row's final sum: a further pass over K recomputes the scores, from
+// the last tile to the first, so that it finds in L2 what the first pass has read last.
+//
+// Measured (B200, inputs changing from pass to pass): 32 sequences of up to 32K tokens, 8 rows a group
+// (762 MB): 127 us a call, the first kernel 117 us = 6.5 TB/s, at the rate of a copy. 1M tokens, 4
+// groups of 32 rows (1.07 GB): 195 us a call on a cool GPU, 240 us in a long run, where the SM clock
+// falls to 1.67 GHz under the power cap (4.5 TB/s): the 32 rows take 1100 to 1250 cycles a tile, the
+// accumulating warps first. With weights, 8 sequences of 64K (454 MB and K again): 118 us, of which 70
+// the first kernel and 32 the pass over K, a third of it from L2. Small calls are launches, one chain of
+// cold loads and instruction fetch: 9 us on the device for 1900 tokens.
+// Not taken: two terms added up in one column of S^T or O^T (the second would need its scale inside the
+// MMA), a maximum carried over from earlier tiles (loses the digits above), converting to fp16 (the
+// conversions alone would take as long as HBM).
 #include <cuda.h>
 
 #include "cache8.cuh"
@@ -49,7 +63,8 @@ struct Cfg {
   static constexpr int kQ = N * D;
   static constexpr int kP = W ? 0 : kTok * N;
   // Softmax groups of four warps, each with a buffer of S^T, P and O^T of its own. Two keep up with
-  // HBM where a tile is 32 KB and has up to 16 rows; 32 rows took 1350 cycles a tile with two.
+  // HBM where a tile is 32 KB and has up to 16 rows; 32 rows took 1350 cycles a tile with two, and
+  // tiles of 16 KB (5000 tokens, 15 rows) 22 us a call instead of 18.
   static constexpr int kGroups = W || D == 64 || NR == 32 ? 3 : 2;
   static constexpr int kThreads = 128 + 128 * kGroups + (W ? 0 : 128);
   static constexpr int kTmemUsed = (W ? 1 : 2) * kGroups * N;
@@ -72,8 +87,9 @@ struct Shared {
   volatile int abort_flag;
   int start_b, start_off, stopped;
   int wsum[32], wmore[32];
-  int nan_any[2];
-  int nan_at[2][128];                      // per head dim: first token not visible to all rows whose V is NaN there
+  // per unit modulo the groups (the softmax warps can be that many units ahead of the accumulating ones):
+  int nan_any[kMaxGroups];
+  int nan_at[kMaxGroups][128];             // per head dim: first token not visible to all rows whose V is NaN there
   int wev[kMaxGroups][4];
   alignas(16) float fac[2][NR];            // per unit parity: 2^e log2 e / sqrt(d) of a row
   float lse[2][NR];
@@ -416,10 +432,10 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
     tc::mbar_init(&sh.f_full[i], 32);
     tc::mbar_init(&sh.o_full[i], 1);
     tc::mbar_init(&sh.o_empty[i], 4);
+    sh.nan_any[i] = 0;
   } else if (tid >= 16 && tid < 18) {
     tc::mbar_init(&sh.q_full[tid - 16], 32 * C::kQWarps);
     tc::mbar_init(&sh.q_empty[tid - 16], 1 + 4 * kGroups);
-    sh.nan_any[tid - 16] = 0;
     sh.abort_flag = 0;
   } else if (tid == 32) {
     tc::prefetch_tensormap(&map_k);
@@ -428,7 +444,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
     sh.stopped = tc::grid_timed_out(a.status);
   }
   if (tid < 18) tc::fence_mbar_init();
-  if (tid < 256) sh.nan_at[tid >> 7][tid & 127] = kNever;
+  if (tid < 128 * kMaxGroups) (&sh.nan_at[0][0])[tid] = kNever;
   // tiles of the first kThreads sequences, a thread each, and of all others
   const int mine = tid < a.batch ? tiles_of(c8_len(a.lens, tid, a.T, a.status)) * units_b : 0;
   int more = 0;
@@ -838,9 +854,9 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
                   const uint32_t code = 0x7Fu << (8 * (e & 3));
                   if ((y[e >> 2] & code) != code) continue;
                   y[e >> 2] &= ~(0xFFu << (8 * (e & 3)));
-                  atomicMin(&sh.nan_at[pb][c * 16 + e], tile * kTok + r);
+                  atomicMin(&sh.nan_at[w.piece % kGroups][c * 16 + e], tile * kTok + r);
                 }
-                sh.nan_any[pb] = 1;
+                sh.nan_any[w.piece % kGroups] = 1;
                 *p = make_uint4(y[0], y[1], y[2], y[3]);
               }
             }
@@ -914,76 +930,76 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
   } else {
     const int q_first = warp - 4 - 4 * kGroups;
     if constexpr (!W) {
-    // ---- a thread per head dim: outputs ----
-    const int q4 = warp & 3, t = tid & 127;
-    const int dim = D == 128 ? t : t & 63, rb = D == 128 ? 0 : (t >> 6) * C::kRowsT;
-    // columns of O^T: rows i q .. of the first terms, then of the second, for i = 0 .. 3
-    const uint32_t to = tmem_o + ((uint32_t)(q4 * 32) << 16) + (uint32_t)(C::kRowsT < 8 ? 0 : 2 * rb);
-    uint64_t o[C::kRowsT / 2];
+      // ---- a thread per head dim: outputs ----
+      const int q4 = warp & 3, t = tid & 127;
+      const int dim = D == 128 ? t : t & 63, rb = D == 128 ? 0 : (t >> 6) * C::kRowsT;
+      // columns of O^T: rows i q .. of the first terms, then of the second, for i = 0 .. 3
+      const uint32_t to = tmem_o + ((uint32_t)(q4 * 32) << 16) + (uint32_t)(C::kRowsT < 8 ? 0 : 2 * rb);
+      uint64_t o[C::kRowsT / 2];
 #pragma unroll
-    for (int r = 0; r < C::kRowsT / 2; ++r) o[r] = 0ull;
-    int sb = 0;
-    uint32_t ph = 0;
-    for (Walk ahead = w; w.left > 0; w = ahead) {
-     walk_next<W>(ahead, a);
-     if (ahead.left > 0) split_piece<D, NR, W>(a, ahead, sh, sQ, q_first, abort, lane);
-     const int pb = w.piece & 1;
-     const long unit = (long)w.b * units_b + w.g * a.nch + w.ch, slot = unit + blockIdx.x;
-     for (int n = w.t1 - w.t0; n > 0; --n) {
-      warp_wait(&sh.f_full[sb], ph, abort, a.status);
-      if (sh.any_fa[sb]) {
+      for (int r = 0; r < C::kRowsT / 2; ++r) o[r] = 0ull;
+      int sb = 0;
+      uint32_t ph = 0;
+      for (Walk ahead = w; w.left > 0; w = ahead) {
+        walk_next<W>(ahead, a);
+        if (ahead.left > 0) split_piece<D, NR, W>(a, ahead, sh, sQ, q_first, abort, lane);
+        const int nb = w.piece % kGroups;
+        const long unit = (long)w.b * units_b + w.g * a.nch + w.ch, slot = unit + blockIdx.x;
+        for (int n = w.t1 - w.t0; n > 0; --n) {
+          warp_wait(&sh.f_full[sb], ph, abort, a.status);
+          if (sh.any_fa[sb]) {
 #pragma unroll
-        for (int r = 0; r < C::kRowsT; r += 2)
-          o[r / 2] = mul2(o[r / 2], *reinterpret_cast<const uint64_t*>(&sh.fa[sb][rb + r]));
-      }
-      warp_wait(&sh.o_full[sb], ph, abort, a.status);
-      tc::fence_after_sync();
+            for (int r = 0; r < C::kRowsT; r += 2)
+              o[r / 2] = mul2(o[r / 2], *reinterpret_cast<const uint64_t*>(&sh.fa[sb][rb + r]));
+          }
+          warp_wait(&sh.o_full[sb], ph, abort, a.status);
+          tc::fence_after_sync();
 #pragma unroll
-      for (int r0 = 0; r0 < C::kRowsT; r0 += 16) {
-        constexpr int kH = C::kRowsT < 16 ? C::kRowsT : 16, q = C::q;
-        uint32_t c[2][16];
-        tc::tmem_ld16_nowait(to + (uint32_t)(sb * C::N + 2 * r0), c[0]);
-        if constexpr (kH == 16) tc::tmem_ld16_nowait(to + (uint32_t)(sb * C::N + 2 * r0 + 16), c[1]);
-        tc::tmem_wait_ld2(c[0], c[1]);
+          for (int r0 = 0; r0 < C::kRowsT; r0 += 16) {
+            constexpr int kH = C::kRowsT < 16 ? C::kRowsT : 16, q = C::q;
+            uint32_t c[2][16];
+            tc::tmem_ld16_nowait(to + (uint32_t)(sb * C::N + 2 * r0), c[0]);
+            if constexpr (kH == 16) tc::tmem_ld16_nowait(to + (uint32_t)(sb * C::N + 2 * r0 + 16), c[1]);
+            tc::tmem_wait_ld2(c[0], c[1]);
 #pragma unroll
-        for (int r = 0; r < kH; r += 2) {
-          const int h = r >> 3, x = (r & 7) / q * 2 * q + (r & 7) % q;
-          float x1 = __uint_as_float(c[h][x]), y1 = __uint_as_float(c[h][x + 1]);
-          float x2 = __uint_as_float(c[h][x + q]), y2 = __uint_as_float(c[h][x + q + 1]);
-          if constexpr (C::kRowsT < 8) {  // the upper rows' threads: 8 columns on
-            if (rb) {
-              x1 = __uint_as_float(c[0][x + 8]), y1 = __uint_as_float(c[0][x + 9]);
-              x2 = __uint_as_float(c[0][x + q + 8]), y2 = __uint_as_float(c[0][x + q + 9]);
+            for (int r = 0; r < kH; r += 2) {
+              const int h = r >> 3, x = (r & 7) / q * 2 * q + (r & 7) % q;
+              float x1 = __uint_as_float(c[h][x]), y1 = __uint_as_float(c[h][x + 1]);
+              float x2 = __uint_as_float(c[h][x + q]), y2 = __uint_as_float(c[h][x + q + 1]);
+              if constexpr (C::kRowsT < 8) {  // the upper rows' threads: 8 columns on
+                if (rb) {
+                  x1 = __uint_as_float(c[0][x + 8]), y1 = __uint_as_float(c[0][x + 9]);
+                  x2 = __uint_as_float(c[0][x + q + 8]), y2 = __uint_as_float(c[0][x + q + 9]);
+                }
+              }
+              const float4 f = sh.fb[sb][(rb + r0 + r) / 2];
+              uint64_t& y = o[(r0 + r) / 2];
+              y = fma2(pack2(x2, y2), pack2(f.z, f.w), fma2(pack2(x1, y1), pack2(f.x, f.y), y));
             }
           }
-          const float4 f = sh.fb[sb][(rb + r0 + r) / 2];
-          uint64_t& y = o[(r0 + r) / 2];
-          y = fma2(pack2(x2, y2), pack2(f.z, f.w), fma2(pack2(x1, y1), pack2(f.x, f.y), y));
-        }
-      }
-      tc::fence_before_sync();
-      if (n == 1) {
-        if (sh.nan_any[pb]) {
-          const int np = sh.nan_at[pb][dim], r0 = w.ch * a.chunk_rows + rb, R = a.Hq / a.G;
+          tc::fence_before_sync();
+          if (n == 1) {
+            if (sh.nan_any[nb]) {
+              const int np = sh.nan_at[nb][dim], r0 = w.ch * a.chunk_rows + rb, R = a.Hq / a.G;
 #pragma unroll
-          for (int r = 0; r < C::kRowsT; r += 2) {
-            const float nan = __int_as_float(0x7FC00000);
-            const float2 y = unpack2(o[r / 2]);
-            o[r / 2] = pack2(np <= w.L - a.n_new + (r0 + r) / R ? nan : y.x,
-                             np <= w.L - a.n_new + (r0 + r + 1) / R ? nan : y.y);
+              for (int r = 0; r < C::kRowsT; r += 2) {
+                const float nan = __int_as_float(0x7FC00000);
+                const float2 y = unpack2(o[r / 2]);
+                o[r / 2] = pack2(np <= w.L - a.n_new + (r0 + r) / R ? nan : y.x,
+                                 np <= w.L - a.n_new + (r0 + r + 1) / R ? nan : y.y);
+              }
+            }
+            group_sync(7);
+            sh.nan_at[nb][t] = kNever;
+            if (t == 0) sh.nan_any[nb] = 0;
+          }
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&sh.o_empty[sb]);
+          if (++sb == kGroups) {
+            sb = 0;
+            ph ^= 1u;
           }
         }
-        group_sync(7);
-        sh.nan_at[pb][t] = kNever;
-        if (t == 0) sh.nan_any[pb] = 0;
-      }
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&sh.o_empty[sb]);
-      if (++sb == kGroups) {
-        sb = 0;
-        ph ^= 1u;
-      }
-     }
         float* po = part.o(slot) + rb * D + dim;
 #pragma unroll
         for (int r = 0; r < C::kRowsT; r += 2) {
@@ -996,7 +1012,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
           if (w.t0 == 0) part.first[unit] = (int)blockIdx.x;
           if (w.t1 == w.ntiles) part.last[unit] = (int)blockIdx.x;
         }
-    }
+      }
     }
   }
   tc::fence_before_sync();

@@ -365,6 +365,29 @@ def test_attend_nan_values_over_two_tiles_of_new_tokens(n_new, L):
     assert torch.equal(torch.nan_to_num(out), torch.nan_to_num(want))
 
 
+@pytest.mark.parametrize("d,R", [(64, 2), (128, 2), (128, 12)])
+def test_attend_nan_values_of_many_short_sequences(d, R):
+    """Every other of 1800 short sequences has a NaN in the V of its last token, each at its own length and dim."""
+    gen = torch.Generator().manual_seed(d + R)
+    batch, n, block, T = 1800, 2, 32, 96
+    lens = [2 + int(x) for x in torch.randint(0, T - 2, (batch,), generator=gen)]
+    c = c8.filled_cache(gen, lens, T, 1, d, block)
+    q, gate = queries(gen, batch, n, R, d)
+    base, _ = check_attend(c8.to_cuda(c), block, lens, q, gate, False)
+    want = base.clone()
+    for b in range(0, batch, 2):
+        c["v8"][b, lens[b] - 1, 0, (7 * b) % d] = 0x7F
+        want[b, 1, :, (7 * b) % d] = math.nan
+    c, dm = c8.to_cuda(c), dims(batch, T, R, 1, d)
+    ws = workspace(dm, block, n)
+    for _ in range(3):
+        out = torch.zeros_like(q)
+        sg.sgqa_cache8_attend(dm, block, i32(lens), n, q, gate, *cache_args(c), out, ws)
+        torch.cuda.synchronize()
+        nan_rows(out, want)
+        assert torch.equal(torch.nan_to_num(out), torch.nan_to_num(want))
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_attend_rows_of_nan_and_infinity(d):
     """A query with a NaN or an infinity gives NaN, its neighbours what they give without it."""
