@@ -5,9 +5,10 @@
 // shared memory, and the codes go out as one 16-byte store per row piece: each new element is read
 // once and written once, no second pass. A block that held tokens before keeps its scale unless a new
 // token needs a larger one; only then are its codes read, rounded again and rewritten. HBM bound: 2
-// bytes read and 1 written per element. (Item indices are 32-bit and the sequence is a grid
-// dimension: with 64-bit divisions the kernel was bound by them, 106 us for 8 prompts of up to 24K
-// tokens, 258 MB.)
+// bytes read and 1 written per element. Item indices are 32-bit, the sequence is a grid dimension and a
+// CTA goes through several items: with 64-bit divisions for every item the kernel was bound by them.
+// Measured: 8 prompts of up to 24K tokens (258 MB) 47 us a call, the kernel 39 us = 6.6 TB/s (105 us
+// before); four tokens of 32 sequences 4.3 us on the device.
 #include "cache8.cuh"
 
 namespace sgqa {

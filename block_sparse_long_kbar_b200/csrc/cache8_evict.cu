@@ -1,5 +1,10 @@
 // Eviction from the block-scaled 8-bit KV cache (format: cache8.cuh) by accumulated attention
 // weight: which tokens stay, and their move to another cache.
+// Bytes: a weight per token and group once, a kept row of K and of V read and written once. Measured: 32
+// sequences of 8K tokens to 4K (277 MB) 66 us a call, of which the selection 13 us and the move 50 us =
+// 5.4 TB/s (rows of 128 bytes, a random half of them); 1M tokens to 131072 (289 MB) 96 us, of which the
+// selection 43 us (five launches over 16 MB of weights, each a chain of load, scan and count) and the
+// move 52 us.
 #include <cooperative_groups.h>
 
 #include "cache8.cuh"
@@ -545,7 +550,7 @@ cudaError_t launch_keep(const C8EvictArgs& a, int ctas, cudaStream_t s) {
 // Which selection: clusters of as few CTAs as hold a (sequence, group)'s weights in registers with four
 // loads a lane, up to 8; of more while that leaves SMs without a CTA and a part 2048 weights or more.
 // Where 8 do not hold them: launches over the whole GPU if clusters of 16 would leave SMs without a CTA
-// (1M weights, 4 groups: 76 us with 4 clusters of 16), else those.
+// (1M weights, 4 groups: 43 us, against 76 us with 4 clusters of 16), else those.
 bool keep_on_grid(long units, int T) { return !keep_fits(T, 4, 8) && units * 16 <= 148; }
 int keep_grid_ctas(int T) { return (int)(((long)T + 6 + 4 * kGridVec * kGridThr - 1) / (4 * kGridVec * kGridThr)); }
 cudaError_t launch_keep_any(const C8EvictArgs& a, cudaStream_t s) {
