@@ -77,6 +77,10 @@ struct Cfg {
 };
 
 constexpr int kMaxGroups = 3;
+// Where a CTA's tiles begin (the weights' pass: end): unit and tile, and how many there are (0: none).
+struct Start {
+  int b, g, ch, L, ntiles, tile, left;
+};
 template <int NR>
 struct Shared {
   uint64_t full[8], empty[8];
@@ -85,7 +89,7 @@ struct Shared {
   float scale[8][32];                      // per stage: K scales of the tile's blocks, then V scales
   uint32_t tmem;
   volatile int abort_flag;
-  int start_b, start_off, stopped;
+  Start start;
   int wsum[32], wmore[32];
   // per unit modulo the groups (the softmax warps can be that many units ahead of the accumulating ones):
   int nan_any[kMaxGroups];
@@ -103,6 +107,15 @@ struct Shared {
   float4 fb[kMaxGroups][NR / 2];
 };
 
+__device__ __forceinline__ int warp_scan(int x, int lane) {
+#pragma unroll
+  for (int h = 1; h < 32; h <<= 1) {
+    const int y = __shfl_up_sync(0xFFFFFFFFu, x, h);
+    if (lane >= h) x += y;
+  }
+  return x;
+}
+
 // The tiles of one CTA in order, a piece of a unit at a time: tiles [t0, t1) of unit ((sequence b,
 // group g), chunk ch of its rows). A loop over a piece's tiles has nothing else to keep track of: with
 // four roles on every scheduler, instruction fetch is what short loops are for. The weights' pass goes
@@ -116,19 +129,101 @@ __device__ __forceinline__ int len_of(const C8AttendArgs& a, int b) {
   const int n = __ldg(a.lens + b);
   return n >= 0 && n <= a.T ? n : 0;
 }
-// off: the CTA's first tile (back: its last one) among the sequence's
 template <bool BACK>
-__device__ __forceinline__ void walk_begin(Walk& w, const C8AttendArgs& a, int b, int off, int left) {
-  w.b = b;
-  w.L = len_of(a, b);
-  w.ntiles = tiles_of(w.L);
-  const int gu = off / w.ntiles, tile = off - gu * w.ntiles;
-  w.g = gu / a.nch;
-  w.ch = gu - w.g * a.nch;
-  w.left = left;
-  w.t0 = BACK ? max(0, tile + 1 - left) : tile;
-  w.t1 = BACK ? tile + 1 : min(w.ntiles, tile + left);
+__device__ __forceinline__ void walk_begin(Walk& w, const Start& s) {
+  w.b = s.b;
+  w.g = s.g;
+  w.ch = s.ch;
+  w.L = s.L;
+  w.ntiles = s.ntiles;
+  w.left = s.left;
+  w.t0 = BACK ? max(0, s.tile + 1 - s.left) : s.tile;
+  w.t1 = BACK ? s.tile + 1 : min(s.ntiles, s.tile + s.left);
   w.piece = w.k = 0;
+}
+// This CTA's share of `total` tiles: [t0, t0 + left). Every CTA below min(CTAs, tiles) has one: the CTAs
+// between a unit's first and last have all written.
+__device__ __forceinline__ int share_of(int total, int& t0) {
+  const int n = min((int)gridDim.x, total), cta = (int)blockIdx.x;
+  if (cta >= n) return 0;
+  const int each = total / n, odd = total - each * n;
+  t0 = each * cta + min(cta, odd);
+  return each + (cta < odd ? 1 : 0);
+}
+// off: the tile's place among those of sequence b
+__device__ __forceinline__ void set_start(Start& s, const C8AttendArgs& a, int b, int L, int off, int left) {
+  s.b = b;
+  s.L = L;
+  s.ntiles = tiles_of(L);
+  const int gu = off / s.ntiles;
+  s.tile = off - gu * s.ntiles;
+  s.g = a.nch == 1 ? gu : gu / a.nch;
+  s.ch = gu - s.g * a.nch;
+  s.left = left;
+}
+// The start, found by one warp from up to 256 lengths. (Short loops: this runs once, from a cold
+// instruction cache, and everything waits for it.)
+constexpr int kWarpLens = 256;
+template <bool BACK>
+__device__ __forceinline__ void warp_start(Start& s, const C8AttendArgs& a, int lane) {
+  const int units_b = a.G * a.nch;
+  int total = 0;
+  const bool stopped = tc::grid_timed_out(a.status);
+#pragma unroll 1
+  for (int b = lane; b < a.batch; b += 32) total += tiles_of(c8_len(a.lens, b, a.T, a.status));
+  total = __reduce_add_sync(0xFFFFFFFFu, total) * units_b;
+  int t0 = 0;
+  const int left = __any_sync(0xFFFFFFFFu, stopped) ? 0 : share_of(total, t0);
+  if (left == 0) {
+    if (lane == 0) s.left = 0;
+    return;
+  }
+  const int from = BACK ? t0 + left - 1 : t0;
+#pragma unroll 1
+  for (int b = lane, seen = 0;; b += 32) {
+    const int L = b < a.batch ? len_of(a, b) : 0, n = tiles_of(L) * units_b;
+    int x = n;
+#pragma unroll 1
+    for (int h = 1; h < 32; h <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, x, h);
+      if (lane >= h) x += y;
+    }
+    x += seen;
+    if (x > from && x - n <= from) set_start(s, a, b, L, from - (x - n), left);
+    seen = __shfl_sync(0xFFFFFFFFu, x, 31);
+    if (seen > from) break;
+  }
+}
+// The start from any number of lengths: all threads of the CTA.
+template <int THREADS, bool BACK, class SH>
+__device__ __forceinline__ void block_start(SH& sh, const C8AttendArgs& a, int tid) {
+  const int warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) sh.wmore[31] = tc::grid_timed_out(a.status);
+  int mine = 0;
+  for (int b = tid; b < a.batch; b += THREADS) mine += tiles_of(c8_len(a.lens, b, a.T, a.status)) * a.G * a.nch;
+  mine = __reduce_add_sync(0xFFFFFFFFu, mine);
+  if (lane == 0) sh.wmore[warp] = mine;
+  __syncthreads();
+  int total = 0, t0 = 0;
+  for (int i = 0; i < THREADS / 32; ++i) total += sh.wmore[i];
+  const int left = sh.wmore[31] ? 0 : share_of(total, t0), from = BACK ? t0 + left - 1 : t0;
+  if (left == 0) {
+    if (tid == 0) sh.start.left = 0;
+    return;
+  }
+  for (int b0 = 0, seen = 0; seen <= from; b0 += THREADS) {
+    const int b = b0 + tid, L = b < a.batch ? len_of(a, b) : 0, n = tiles_of(L) * a.G * a.nch;
+    int x = warp_scan(n, lane);
+    __syncthreads();
+    if (lane == 31) sh.wsum[warp] = x;
+    __syncthreads();
+    x += seen;
+    for (int i = 0; i < THREADS / 32; ++i) {
+      if (i < warp) x += sh.wsum[i];
+      seen += sh.wsum[i];
+    }
+    if (x > from && x - n <= from) set_start(sh.start, a, b, L, from - (x - n), left);
+  }
 }
 template <bool BACK>
 __device__ __forceinline__ void walk_next(Walk& w, const C8AttendArgs& a) {
@@ -300,15 +395,6 @@ __device__ __forceinline__ void warp_wait(uint64_t* bar, uint32_t parity, volati
   __syncwarp();
 }
 
-__device__ __forceinline__ int warp_scan(int x, int lane) {
-#pragma unroll
-  for (int h = 1; h < 32; h <<= 1) {
-    const int y = __shfl_up_sync(0xFFFFFFFFu, x, h);
-    if (lane >= h) x += y;
-  }
-  return x;
-}
-
 // x[j] over the eight lanes that share rows (lane / 4), joined by op in a fixed order; the lane gets
 // row (lane / 4) mod Q.
 template <int Q, class Op>
@@ -421,87 +507,56 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
 
   grid_dependents();  // (the kernels behind wait for this one's end where they need it)
   // ---- barriers; this CTA's piece of the tiles ----
-  if (tid < 8) {
-    tc::mbar_init(&sh.full[tid], 1 + 32);
-    tc::mbar_init(&sh.empty[tid], W ? 1 + 4 : 1);  // the weights' pass reads scales after the MMA
-  } else if (tid < 8 + kGroups) {
-    const int i = tid - 8;
-    tc::mbar_init(&sh.s_full[i], 1);
-    tc::mbar_init(&sh.s_empty[i], 4);
-    tc::mbar_init(&sh.p_full[i], 128);
-    tc::mbar_init(&sh.f_full[i], 32);
-    tc::mbar_init(&sh.o_full[i], 1);
-    tc::mbar_init(&sh.o_empty[i], 4);
-    sh.nan_any[i] = 0;
-  } else if (tid >= 16 && tid < 18) {
-    tc::mbar_init(&sh.q_full[tid - 16], 32 * C::kQWarps);
-    tc::mbar_init(&sh.q_empty[tid - 16], 1 + 4 * kGroups);
-    sh.abort_flag = 0;
-  } else if (tid == 32) {
-    tc::prefetch_tensormap(&map_k);
-    if (!W) tc::prefetch_tensormap(&map_v);
-  } else if (tid == 64) {
-    sh.stopped = tc::grid_timed_out(a.status);
+  // The first warp makes what it needs by itself and goes on to fetch the first tiles, while the others
+  // wait for what it leaves behind. (Lengths of more sequences than a warp reads: all together.)
+  if (a.batch > kWarpLens) {
+    block_start<kThreads, W>(sh, a, tid);
+    __syncthreads();
   }
-  if (tid < 18) tc::fence_mbar_init();
-  if (tid < 128 * kMaxGroups) (&sh.nan_at[0][0])[tid] = kNever;
-  // tiles of the first kThreads sequences, a thread each, and of all others
-  const int mine = tid < a.batch ? tiles_of(c8_len(a.lens, tid, a.T, a.status)) * units_b : 0;
-  int more = 0;
-  for (int b = tid + kThreads; b < a.batch; b += kThreads) more += tiles_of(c8_len(a.lens, b, a.T, a.status)) * units_b;
-  more = __reduce_add_sync(0xFFFFFFFFu, more);
-  int upto = warp_scan(mine, lane);
-  if (lane == 31) {
-    sh.wsum[warp] = upto;
-    sh.wmore[warp] = more;
+  if (warp == 0) {
+    if (lane < 8) {
+      tc::mbar_init(&sh.full[lane], 1 + 32);
+      tc::mbar_init(&sh.empty[lane], W ? 1 + 4 : 1);  // the weights' pass reads scales after the MMA
+    } else if (lane < 8 + kGroups) {
+      const int i = lane - 8;
+      tc::mbar_init(&sh.s_full[i], 1);
+      tc::mbar_init(&sh.s_empty[i], 4);
+      tc::mbar_init(&sh.p_full[i], 128);
+      tc::mbar_init(&sh.f_full[i], 32);
+      tc::mbar_init(&sh.o_full[i], 1);
+      tc::mbar_init(&sh.o_empty[i], 4);
+    } else if (lane >= 16 && lane < 18) {
+      tc::mbar_init(&sh.q_full[lane - 16], 32 * C::kQWarps);
+      tc::mbar_init(&sh.q_empty[lane - 16], 1 + 4 * kGroups);
+    } else if (lane == 18) {
+      sh.abort_flag = 0;
+    }
+    tc::fence_mbar_init();
+    if (a.batch <= kWarpLens) warp_start<W>(sh.start, a, lane);
+    __syncwarp();
+    asm volatile("bar.arrive 9, %0;" ::"n"(kThreads) : "memory");
+  } else {
+    if (warp == 1) tc::tmem_alloc(&sh.tmem, C::kTmem);
+    if (tid == 64) {
+      tc::prefetch_tensormap(&map_k);
+      if (!W) tc::prefetch_tensormap(&map_v);
+    }
+    if (tid >= 128 && tid < 128 + 128 * kMaxGroups) (&sh.nan_at[0][0])[tid - 128] = kNever;
+    if (tid >= 96 && tid < 96 + kMaxGroups) sh.nan_any[tid - 96] = 0;
+    tc::fence_before_sync();
+    asm volatile("bar.sync 9, %0;" ::"n"(kThreads) : "memory");
+    tc::fence_after_sync();
   }
-  __syncthreads();
-  int total = 0, seen = 0;
-#pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) {
-    if (i < warp) upto += sh.wsum[i];
-    seen += sh.wsum[i];
-    total += sh.wmore[i];
-  }
-  total += seen;
-  // (every CTA below n has a tile: the CTAs between a unit's first and last have all written)
-  const int n = min((int)gridDim.x, total), cta = (int)blockIdx.x;
-  if (cta >= n || sh.stopped) {
+  if (sh.start.left == 0) {
     if (W) grid_wait();  // (no kernel ends before the one it was started behind)
+    if (warp == 1) tc::tmem_dealloc(sh.tmem, C::kTmem);
     return;
   }
-  const int each = total / n, odd = total - each * n;
-  const int t0 = each * cta + min(cta, odd), t1 = t0 + each + (cta < odd ? 1 : 0);
-  if (warp == 1) tc::tmem_alloc(&sh.tmem, C::kTmem);
-  const int from = W ? t1 - 1 : t0;
-  if (upto > from && upto - mine <= from) {
-    sh.start_b = tid;
-    sh.start_off = from - (upto - mine);
-  }
-  for (int b0 = kThreads; seen <= from; b0 += kThreads) {
-    const int b = b0 + tid, nb = b < a.batch ? tiles_of(len_of(a, b)) * units_b : 0;
-    int x = warp_scan(nb, lane);
-    __syncthreads();
-    if (lane == 31) sh.wsum[warp] = x;
-    __syncthreads();
-    x += seen;
-    for (int i = 0; i < kThreads / 32; ++i) {
-      if (i < warp) x += sh.wsum[i];
-      seen += sh.wsum[i];
-    }
-    if (x > from && x - nb <= from) {
-      sh.start_b = b;
-      sh.start_off = from - (x - nb);
-    }
-  }
-  tc::fence_before_sync();
-  __syncthreads();
-  tc::fence_after_sync();
-  const uint32_t tmem = sh.tmem;
+  const uint32_t tmem = warp == 0 ? 0u : sh.tmem;  // (the first warp may be ahead of its allocation)
   const uint32_t tmem_o = tmem + kGroups * C::N;
   volatile int* abort = &sh.abort_flag;
   Walk w;
-  walk_begin<W>(w, a, sh.start_b, sh.start_off, t1 - t0);
+  walk_begin<W>(w, sh.start);
   const Part<D, NR> part(a.part, (long)a.batch * units_b);
 
   // the first piece's rows of q: all warps but those that have tiles to fetch and to multiply
