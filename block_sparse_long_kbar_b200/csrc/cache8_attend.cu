@@ -575,8 +575,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
   if (warp == 0 || (C::kFetch == 2 && warp == 2)) {
     // ---- TMA: K and V tiles; a lane per block: their scales ----
     const int me = warp >> 1;
-    const long nblk = ((long)a.T + a.block - 1) >> a.block_log2;
-    const int per = kTok >> a.block_log2, part_v = lane >> 4, j = lane & 15;
+    const int nblk = (a.T + a.block - 1) >> a.block_log2, per = kTok >> a.block_log2;  // (batch * T * G is below 2^31)
+    const int part_v = lane >> 4, j = lane & 15;
     const float* scales = part_v ? a.c.vs : a.c.ks;
     const bool mine = j < per && !(W && part_v);
     int issued = 0, st = me;
@@ -584,8 +584,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
     bool stop = !W && (int)blockIdx.x == a.stall_cta;
     const uint64_t once = evict_first_policy();  // V where K is read again for the weights
     for (; w.left > 0 && !stop; walk_next<W>(w, a)) {
-      const float* src = scales + ((long)w.b * nblk + j) * a.G + w.g;
-      const int z = w.b * a.T;
+      const int src = (w.b * nblk + j) * a.G + w.g, z = w.b * a.T;
       for (int x = (me + C::kFetch - w.k % C::kFetch) % C::kFetch; x < w.t1 - w.t0; x += C::kFetch) {
         const int tile = walk_tile<W>(w, x);
         if (w.k + x >= C::kStages) {
@@ -603,8 +602,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
             tc::tma_load_3d(dst + C::kTile, &map_v, &sh.full[st], 0, w.g, z + tile * kTok);
           }
         }
-        const long blk = (long)tile * per;
-        if (mine && blk + j < nblk) cp_async4(&sh.scale[st][lane], src + blk * a.G);
+        const int blk = tile * per;
+        if (mine && blk + j < nblk) cp_async4(&sh.scale[st][lane], scales + (src + blk * a.G));
         cp_async_arrive(&sh.full[st]);
         issued = w.k + x + 1;
         st += C::kFetch;
