@@ -14,7 +14,7 @@ namespace cg = cooperative_groups;
 namespace sgqa {
 namespace {
 
-constexpr int kSelThr = 1024;
+constexpr int kSelThr = 512;           // (1024: 11.1 instead of 9.7 us for 3 sequences of 777, no less for 8K)
 constexpr int kSelPart = 4 * kSelThr;  // weights of a CTA per 16-byte load of its threads
 
 // Words of global memory that the selection over the whole GPU has per unit.
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kSelThr) cache8_keep_kernel(C8EvictArgs a) {
   const int L = c8_len(a.lens, unit / a.G, a.T, a.status);
   if (keep_simple(a, unit, L, rank * kSelThr + tid, ctas * kSelThr)) return;
   Part<VEC> part;
-  part.set(a, unit, L - a.recent, ctas, rank, 32);
+  part.set(a, unit, L - a.recent, ctas, rank, kSelThr / 32);
   // a pass over the part: take(base) with the keys of vectors base ..
   auto pass_over = [&](auto&& take) {
     if (REG) {
@@ -249,11 +249,13 @@ __global__ void __launch_bounds__(kSelThr) cache8_keep_kernel(C8EvictArgs a) {
   for (int pass = 0; pass < 3; ++pass) {
     pass_over([&](int) { part.count(hist[pass], pass, prefix); });
     cluster.sync();
-    uint32_t bins[2] = {0u, 0u};
+    uint32_t bins[4] = {0u, 0u, 0u, 0u};
     for (int r = 0; r < ctas; ++r) {
-      const uint2 h = *cluster.map_shared_rank(reinterpret_cast<uint2*>(&hist[pass][2046 - 2 * tid]), r);
-      bins[0] += h.y;
-      bins[1] += h.x;
+      const uint4 h = *cluster.map_shared_rank(reinterpret_cast<uint4*>(&hist[pass][2044 - 4 * tid]), r);
+      bins[0] += h.w;
+      bins[1] += h.z;
+      bins[2] += h.y;
+      bins[3] += h.x;
     }
     find_bin(bins, pass, prefix, need, buf, found);
   }
@@ -547,11 +549,11 @@ cudaError_t launch_keep(const C8EvictArgs& a, int ctas, cudaStream_t s) {
   }
   return cudaLaunchKernelEx(&cfg, cache8_keep_kernel<VEC, REG>, a);
 }
-// Which selection: clusters of as few CTAs as hold a (sequence, group)'s weights in registers with four
+// Which selection: clusters of as few CTAs as hold a (sequence, group)'s weights in registers with eight
 // loads a lane, up to 8; of more while that leaves SMs without a CTA and a part 2048 weights or more.
 // Where 8 do not hold them: launches over the whole GPU if clusters of 16 would leave SMs without a CTA
 // (1M weights, 4 groups: 43 us, against 76 us with 4 clusters of 16), else those.
-bool keep_on_grid(long units, int T) { return !keep_fits(T, 4, 8) && units * 16 <= 148; }
+bool keep_on_grid(long units, int T) { return !keep_fits(T, 8, 8) && units * 16 <= 148; }
 int keep_grid_ctas(int T) { return (int)(((long)T + 6 + 4 * kGridVec * kGridThr - 1) / (4 * kGridVec * kGridThr)); }
 cudaError_t launch_keep_any(const C8EvictArgs& a, cudaStream_t s) {
   const long units = (long)a.batch * a.G;
@@ -568,10 +570,11 @@ cudaError_t launch_keep_any(const C8EvictArgs& a, cudaStream_t s) {
     return launch_behind(cache8_keep_grid_kernel<4>, grid, kGridThr, 0, s, true, a);
   }
   int c = 1;
-  while (c < 8 && (!keep_fits(a.T, 4, c) || (units * c * 2 <= 148 && a.T >= c * 2 * 2048))) c *= 2;
+  while (c < 8 && (!keep_fits(a.T, 8, c) || (units * c * 2 <= 148 && a.T >= c * 2 * 2048))) c *= 2;
   if (keep_fits(a.T, 1, c)) return launch_keep<1, true>(a, c, s);
   if (keep_fits(a.T, 2, c)) return launch_keep<2, true>(a, c, s);
   if (keep_fits(a.T, 4, c)) return launch_keep<4, true>(a, c, s);
+  if (keep_fits(a.T, 8, c)) return launch_keep<8, true>(a, c, s);
   return launch_keep<4, false>(a, 16, s);
 }
 

@@ -613,10 +613,10 @@ def same_eviction(got, c, w, lens, keep, recent, block):
                 assert torch.equal(c8.decode(got[codes][b, :m, g]), want)
 
 
-# one CTA per (sequence, group) with 1, 2 and 4 loads a lane; clusters of 2, 4, 8; of 16; the whole GPU
+# one CTA per (sequence, group) with 1, 2, 4 and 8 loads a lane; clusters of 2, 4, 8; of 16; the whole GPU
 @pytest.mark.parametrize("batch,G,T,keep,recent", [
-    (1, 1, 1, 1, 0), (60, 2, 4096, 1000, 3), (80, 1, 8191, 4000, 0), (75, 1, 16380, 8000, 100), (75, 1, 16381, 700, 1),
-    (1, 2, 5003, 1234, 17), (2, 1, 9002, 8999, 2), (1, 1, 20001, 333, 333), (1, 1, 131071, 60000, 5),
+    (1, 1, 1, 1, 0), (80, 1, 2041, 500, 0), (60, 2, 4096, 1000, 3), (80, 1, 8191, 4000, 0), (75, 1, 16380, 8000, 100),
+    (75, 1, 16381, 700, 1), (1, 2, 5003, 1234, 17), (2, 1, 9002, 8999, 2), (1, 1, 20001, 333, 333), (1, 1, 131071, 60000, 5),
     (5, 2, 140003, 70001, 1000), (3, 1, 131073, 1, 0), (1, 1, 500002, 1000, 0)])
 def test_evict_every_selection(batch, G, T, keep, recent):
     gen = torch.Generator(device="cuda").manual_seed(T)
