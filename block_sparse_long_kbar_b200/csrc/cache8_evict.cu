@@ -1,10 +1,10 @@
 // Eviction from the block-scaled 8-bit KV cache (format: cache8.cuh) by accumulated attention
 // weight: which tokens stay, and their move to another cache.
 // Bytes: a weight per token and group once, a kept row of K and of V read and written once. Measured: 32
-// sequences of 8K tokens to 4K (277 MB) 66 us a call, of which the selection 13 us and the move 50 us =
-// 5.4 TB/s (rows of 128 bytes, a random half of them); 1M tokens to 131072 (289 MB) 96 us, of which the
-// selection 43 us (five launches over 16 MB of weights, each a chain of load, scan and count) and the
-// move 52 us.
+// sequences of 8K tokens to 4K (277 MB) 59 us on the device, of which the selection 13 us and the move 47
+// us = 5.8 TB/s (rows of 128 bytes, a random half of them); 1M tokens to 131072 (289 MB) 85 us, of which
+// the selection 38 us (five launches over 16 MB of weights, each a chain of load, scan and count) and
+// the move 48 us.
 #include <cooperative_groups.h>
 
 #include "cache8.cuh"
@@ -377,7 +377,8 @@ __device__ __forceinline__ uint32_t amax16(const uint4& x, float scale) {
   return __float_as_uint(c8_decode2(m).x * scale);
 }
 // One item per block of the new cache and group, rows and items as in the append kernel. HBM bound: a
-// kept row is read and written once.
+// kept row is read and written once (with streaming stores: 59 us a call instead of 63 for 32 sequences of
+// 8K, of which the write-back of ordinary ones took the difference).
 constexpr int kLoop = 8;
 template <int D, int BLK>
 __global__ void __launch_bounds__(kThr, BLK * D == 128 * 128 ? 4 : 0) cache8_move_kernel(C8EvictArgs a, int loop) {
@@ -435,8 +436,8 @@ __global__ void __launch_bounds__(kThr, BLK * D == 128 * 128 ? 4 : 0) cache8_mov
         if (z.u[p] >= 0) {
           const long src = (long)((b * a.T + z.u[p]) * a.G + z.g) * D + col;
           const long si = (long)(b * nblk + z.u[p] / BLK) * a.G + z.g;
-          z.xk[p] = __ldg(reinterpret_cast<const uint4*>(a.src.k8 + src));
-          z.xv[p] = __ldg(reinterpret_cast<const uint4*>(a.src.v8 + src));
+          z.xk[p] = __ldcs(reinterpret_cast<const uint4*>(a.src.k8 + src));
+          z.xv[p] = __ldcs(reinterpret_cast<const uint4*>(a.src.v8 + src));
           z.ek[p] = c8_scale_exponent(__ldg(a.src.ks + si));
           z.ev[p] = c8_scale_exponent(__ldg(a.src.vs + si));
         }
@@ -479,8 +480,8 @@ __global__ void __launch_bounds__(kThr, BLK * D == 128 * 128 ? 4 : 0) cache8_mov
       for (int p = 0; p < kPass; ++p) {
         if (z.u[p] < 0) break;
         const long dst = (long)((b * a.T_out + z.j * BLK + row0 + p * kRows) * a.G + z.g) * D + col;
-        *reinterpret_cast<uint4*>(a.dst.k8 + dst) = c8_rescale16(z.xk[p], z.ek[p] - nk);
-        *reinterpret_cast<uint4*>(a.dst.v8 + dst) = c8_rescale16(z.xv[p], z.ev[p] - nv);
+        __stcs(reinterpret_cast<uint4*>(a.dst.k8 + dst), c8_rescale16(z.xk[p], z.ek[p] - nk));
+        __stcs(reinterpret_cast<uint4*>(a.dst.v8 + dst), c8_rescale16(z.xv[p], z.ev[p] - nv));
       }
       if (row0 == 0 && col == 0 && z.u[0] >= 0) {
         const long so = (long)(b * nblk_out + z.j) * a.G + z.g;
@@ -552,7 +553,7 @@ cudaError_t launch_keep(const C8EvictArgs& a, int ctas, cudaStream_t s) {
 // Which selection: clusters of as few CTAs as hold a (sequence, group)'s weights in registers with eight
 // loads a lane, up to 8; of more while that leaves SMs without a CTA and a part 2048 weights or more.
 // Where 8 do not hold them: launches over the whole GPU if clusters of 16 would leave SMs without a CTA
-// (1M weights, 4 groups: 43 us, against 76 us with 4 clusters of 16), else those.
+// (1M weights, 4 groups: 38 us, against 76 us with 4 clusters of 16), else those.
 bool keep_on_grid(long units, int T) { return !keep_fits(T, 8, 8) && units * 16 <= 148; }
 int keep_grid_ctas(int T) { return (int)(((long)T + 6 + 4 * kGridVec * kGridThr - 1) / (4 * kGridVec * kGridThr)); }
 cudaError_t launch_keep_any(const C8EvictArgs& a, cudaStream_t s) {
