@@ -30,15 +30,15 @@
 // the last tile to the first, so that it finds in L2 what the first pass has read last.
 //
 // Measured (B200, inputs changing from pass to pass): 32 sequences of up to 32K tokens, 8 rows a group
-// (762 MB): 127 us a call, the first kernel 117 us = 6.5 TB/s, at the rate of a copy. 1M tokens, 4
-// groups of 32 rows (1.07 GB): 195 us a call on a cool GPU, 240 us in a long run, where the SM clock
+// (762 MB): 126 us a call, the first kernel 118 us = 6.5 TB/s, at the rate of a copy. 1M tokens, 4
+// groups of 32 rows (1.07 GB): 195 us a call on a cool GPU, 235 us in a long run, where the SM clock
 // falls to 1.67 GHz under the power cap (4.5 TB/s): the 32 rows take 1100 to 1250 cycles a tile, the
-// accumulating warps first. With weights, 8 sequences of 64K (454 MB and K again): 118 us, of which 70
+// accumulating warps first. With weights, 8 sequences of 64K (454 MB and K again): 117 us, of which 70
 // the first kernel and 32 the pass over K, a third of it from L2. Small calls are launches, one chain of
-// cold loads and instruction fetch: 9 us on the device for 1900 tokens.
+// cold loads and instruction fetch: 8 us on the device for 1900 tokens.
 // Not taken: two terms added up in one column of S^T or O^T (the second would need its scale inside the
-// MMA), a maximum carried over from earlier tiles (loses the digits above), converting to fp16 (the
-// conversions alone would take as long as HBM).
+// MMA), a maximum carried over from earlier tiles (loses the digits above), converting to fp16 (0.4
+// us of a tile's 0.75 for the conversions alone, and twice the shared memory).
 #include <cuda.h>
 
 #include "cache8.cuh"
