@@ -630,6 +630,25 @@ def test_evict_every_selection(batch, G, T, keep, recent):
     same_eviction(got, c, w, lens, keep, recent, 32)
 
 
+# many groups; one token; lengths of as many sequences as one warp or one CTA reads, and one more
+@pytest.mark.parametrize("batch,G,d,R,n_new,T", [
+    (2, 128, 128, 16, 4, 200), (2, 128, 64, 1, 1, 200), (1, 64, 128, 3, 2, 300), (1, 1, 64, 1, 1, 1), (3, 4, 128, 8, 4, 1),
+    (256, 2, 64, 4, 2, 150), (257, 1, 128, 8, 4, 130), (512, 1, 128, 4, 1, 140), (513, 2, 64, 1, 1, 129), (641, 1, 64, 2, 1, 150)])
+def test_attend_shapes_at_the_limits(batch, G, d, R, n_new, T):
+    gen = torch.Generator(device="cuda").manual_seed(batch + G)
+    cpu, block = torch.Generator().manual_seed(T), 16
+    lens = [int(x) for x in torch.randint(0, T + 1, (batch,), generator=cpu)]
+    lens[-1] = T
+    c = random_codes(gen, batch, T, G, d, block)
+    for n in ("k8", "v8"):
+        c[n] = torch.where(c[n] >= 0x50, c[n] & 0x9F | 0x80, c[n])  # both signs, magnitudes below 2
+        for b, L in enumerate(lens):
+            c[n][b, L:] = 0x7F
+    q, gate = queries(cpu, batch, n_new, G * R, d)
+    w = torch.rand((batch, G, T), generator=gen, device="cuda")
+    check_attend(c, block, lens, q, gate, True, w)
+
+
 @pytest.mark.parametrize("T,keep", [(3000, 500), (150000, 9000)])
 def test_a_captured_eviction_serves_every_length(T, keep):
     gen = torch.Generator(device="cuda").manual_seed(T + 1)
