@@ -8,10 +8,13 @@
 // or head dims), and the few query rows of a (sequence, group) are the narrow one:
 //   S^T[128 tokens x 2 NR] = K_tile . [q1; q2]^T       q = (q1 + q2 / 16) 2^e, both E4M3
 //   O^T[d x 2 NR]          = V_tile^T . [P1 | P2]      p t = (P1 + P2 / 28) 2^E / 448, both E4M3
-// Two E4M3 terms hold q exactly down to 2^-14 of its row's largest element and p t to 2^-8 of itself
-// or 2^-23 of the tile's largest. P is relative to its own tile's maxima (of z per row, of t over the
-// tile), so O^T starts anew in every tile and is added up in registers in fp32: a token that takes
-// nearly all attention costs the far ones none of their digits. The denominator and the maxima are
+// Two E4M3 terms hold q exactly down to 2^-14 of its row's largest element and p t to 1/289 of itself
+// or, where they are subnormal, 2^-23 of 2^E. 2^E is at most 16 times the row's own largest p t of the
+// tile: where the V scales of a tile's blocks are within 2^kSpread of one another it is the tile's largest,
+// against the row's largest p; else a further pass over the scores finds every row's own, since a block of
+// a far larger scale that the row does not see, or hardly, would take the digits of the others. P and E
+// belong to one tile, so O^T starts anew in every tile and is added up in registers in fp32: a token that
+// takes nearly all attention costs the far ones none of their digits. The denominator and the maxima are
 // taken from fp32 scores.
 //
 // Work: the tiles of 128 tokens of all (sequence, group) units, in that order, cut into one equal
@@ -53,6 +56,7 @@ constexpr int kTok = 128;                           // tokens per tile
 constexpr int kGridMax = 148;                       // one CTA per SM
 constexpr int kMaxNR = 32;                          // rows per unit; more make several units
 constexpr int kNever = 0x7FFFFFFF;
+constexpr int kSpread = 4;  // of a tile's V exponents, up to which its rows share a reference
 
 template <int D, int NR, bool W>
 struct Cfg {
@@ -94,12 +98,15 @@ struct Shared {
   // per unit modulo the groups (the softmax warps can be that many units ahead of the accumulating ones):
   int nan_any[kMaxGroups];
   int nan_at[kMaxGroups][128];             // per head dim: first token not visible to all rows whose V is NaN there
-  int wev[kMaxGroups][4];
+  int2 wev[kMaxGroups][4];  // per softmax group and warp: largest and smallest V exponent of its tokens
   alignas(16) float fac[2][NR];            // per unit parity: 2^e log2 e / sqrt(d) of a row
   float lse[2][NR];
   int lim[2][NR];                          // a row's own position; -1: no row
   alignas(16) float wmax[kMaxGroups][4][NR];    // per softmax group and warp: a row's maximum over the tile
   alignas(16) float wsum_p[kMaxGroups][4][NR];  // and the sum of its probabilities
+  // where V's exponents differ: a row's largest score (less the row's maximum) plus V exponent, and over the group
+  alignas(16) float wref[kMaxGroups][4][NR];
+  int ref[kMaxGroups][NR];
   // per softmax group, for the accumulating warps: factors of the sums so far, and whether any is not 1;
   // of this tile's first (x, y) and second (z, w) terms for pairs of rows
   alignas(16) float fa[kMaxGroups][NR];
@@ -253,7 +260,7 @@ __device__ __forceinline__ int walk_tile(const Walk& w, int x) { return BACK ? w
 // Per launch: partial sums of every piece, and the CTAs that hold a unit's first and last tile.
 template <int D, int NR>
 struct Part {
-  static constexpr long kRec = (long)NR * D + NR * 2 + 4;  // O, M, l; E
+  static constexpr long kRec = (long)NR * D + NR * 3;  // O; M, l, E
   float* base;
   int* first;
   int* last;
@@ -394,6 +401,14 @@ __device__ __forceinline__ void warp_wait(uint64_t* bar, uint32_t parity, volati
   if (!tc::mbar_try_wait(bar, parity)) slow_wait(bar, parity, abort, status);
   __syncwarp();
 }
+
+// Exponents (largest, smallest) of V over a tile, from those of a group's warps.
+__device__ __forceinline__ int2 spread_of(const int2 (&w)[4]) {
+  return make_int2(max(max(w[0].x, w[1].x), max(w[2].x, w[3].x)), min(min(w[0].y, w[1].y), min(w[2].y, w[3].y)));
+}
+// A row's sums are held in units of 2^(m + e): m its largest score so far, e an integer with 2^(m + e) at least
+// the references of what it holds. x: such a sum of m and e, less the new m.
+__device__ __forceinline__ int ref_of(float x) { return max(-126, __float2int_ru(x)); }
 
 // x[j] over the eight lanes that share rows (lane / 4), joined by op in a fixed order; the lane gets
 // row (lane / 4) mod Q.
@@ -706,28 +721,30 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
     {
       // ---- a lane per row: running maxima, denominators, factors for the accumulating warps ----
       float m_run = kNegMax, l = 0.f;
-      int e_run = -126, sb = 0;
+      int e_run = -126, sb = 0;  // (the row's)
       uint32_t ph = 0;
       for (; w.left > 0; walk_next<W>(w, a)) {
         for (int n = w.t1 - w.t0; n > 0; --n) {
           warp_wait(&sh.p_full[sb], ph, abort, a.status);
           float now = 1.f;
-          const int et = max(max(sh.wev[sb][0], sh.wev[sb][1]), max(sh.wev[sb][2], sh.wev[sb][3])), en = max(e_run, et);
+          const int2 ev = spread_of(sh.wev[sb]);
           if (lane < NR) {
             const float(&wm)[4][NR] = sh.wmax[sb];
             const float(&ws)[4][NR] = sh.wsum_p[sb];
             const float mt = fmaxf(fmaxf(wm[0][lane], wm[1][lane]), fmaxf(wm[2][lane], wm[3][lane]));
-            const float mn = fmaxf(m_run, mt), fa = ex2_approx(m_run - mn), fb = ex2_approx(mt - mn);
-            const float b = fb * c8_pow2(max(-126, et - en)) * (1.f / 448.f);
+            const float mn = fmaxf(m_run, mt), da = m_run - mn, db = mt - mn;
+            const int et = ev.x - ev.y > kSpread ? sh.ref[sb][lane] : ev.x;
+            const int en = max(ref_of(da + (float)e_run), ref_of(db + (float)et));
+            const float b = ex2_approx(db + (float)(et - en)) * (1.f / 448.f);
             float* f = reinterpret_cast<float*>(&sh.fb[sb][lane >> 1]) + (lane & 1);
             f[0] = b;
             f[2] = b * (1.f / 28.f);
-            now = fa * c8_pow2(max(-126, e_run - en));
+            now = ex2_approx(da + (float)(e_run - en));
             sh.fa[sb][lane] = now;
-            l = fmaf(l, fa, ((ws[0][lane] + ws[1][lane]) + (ws[2][lane] + ws[3][lane])) * fb);
+            l = fmaf(l, ex2_approx(da), ((ws[0][lane] + ws[1][lane]) + (ws[2][lane] + ws[3][lane])) * ex2_approx(db));
             m_run = mn;
+            e_run = en;
           }
-          e_run = en;
           const bool any = __any_sync(0xFFFFFFFFu, now != 1.f);
           if (lane == 0) sh.any_fa[sb] = any;
           tc::mbar_arrive(&sh.f_full[sb]);
@@ -740,8 +757,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
         if (lane < NR) {
           part.m(slot)[lane] = m_run;
           part.l(slot)[lane] = l;
+          part.e(slot)[lane] = e_run;
         }
-        if (lane == 0) *part.e(slot) = e_run;
         m_run = kNegMax;
         l = 0.f;
         e_run = -126;
@@ -783,7 +800,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
         warp_wait(&sh.full[st], ph, abort, a.status);
         tc::fence_after_sync();
         float sk[4];
-        int ev[4], we = -127;
+        int ev[4], we = -127, wl = 127;
         const int sb = tok >> a.block_log2;
         sk[0] = sh.scale[st][sb];
         ev[0] = W ? 0 : (int)(__float_as_uint(sh.scale[st][16 + sb]) >> 23 & 255u) - 127;
@@ -805,6 +822,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
           if (edge && u0 + 8 * e >= w.L) {  // whatever lies behind the last token
             sk[e] = 0.f;
             ev[e] = -127;
+          } else {
+            wl = min(wl, ev[e]);
           }
           we = max(we, ev[e]);
         }
@@ -882,10 +901,11 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
           }
           const float mine = across_tokens<q>(mx, lane, [](float x, float y) { return fmaxf(x, y); });
           we = __reduce_max_sync(0xFFFFFFFFu, we);
+          wl = __reduce_min_sync(0xFFFFFFFFu, wl);
           // the P buffer and the numbers of the tile two tiles back have been read
           if (kp > 0) warp_wait(&sh.o_empty[wg], (kp & 1u) ^ 1u, abort, a.status);
           if ((lane >> 2) < q) sh.wmax[wg][q4][row0 + (lane >> 2)] = mine;
-          if (lane == 0) sh.wev[wg][q4] = we;
+          if (lane == 0) sh.wev[wg][q4] = make_int2(we, wl);
           if (edge) {
             // A zero probability must not meet a NaN code: rows behind the last token become zeros,
             // and a NaN of a token that some row does not see is noted and taken out; the rows that
@@ -929,28 +949,20 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
             mt[j] = pack2(-x.x, -x.y);
             ps[j] = 0ull;
           }
-          const int et = max(max(sh.wev[wg][0], sh.wev[wg][1]), max(sh.wev[wg][2], sh.wev[wg][3]));
+          const int2 es = spread_of(sh.wev[wg]);
           uint8_t* pd = sP + wg * C::kP + (i * 2 * q / 16) * 2048 + (i * 2 * q % 16) + tok * 16;
           const __half2 c28 = __floats2half2_rn(28.f, 28.f);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float cs = 448.f * c8_pow2(max(-126, ev[e] - et));
-            const uint64_t c2 = pack2(cs, cs);
-            uint32_t p1[q / 2], p2[q / 2];  // two codes each
-#pragma unroll
-            for (int j = 0; j < q / 2; ++j) {
-              const float2 x = unpack2(add2(z[e][j], mt[j]));
-              const uint64_t p = pack2(ex2_approx(x.x), ex2_approx(x.y));
-              ps[j] = add2(ps[j], p);
-              const float2 y = unpack2(mul2(p, c2));
-              // Both terms from y rounded to fp16 (2^-11 of itself): the first's rest is exact there (a
-              // multiple of y's last bit, at most 2^-4 of it), and so is its 28-fold.
-              const __half2 h = __floats2half2_rn(y.x, y.y);
-              p1[j] = __nv_cvt_halfraw2_to_fp8x2(h, __NV_SATFINITE, __NV_E4M3);
-              const __half2_raw f = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)p1[j], __NV_E4M3);
-              p2[j] = __nv_cvt_halfraw2_to_fp8x2(__hmul2(__hsub2(h, __half2(f)), c28), __NV_SATFINITE, __NV_E4M3);
-            }
-            uint8_t* d = pd + e * 128;
+          // y (448 p t over the reference) of a token's rows as two terms. Both from y rounded to fp16 (2^-11
+          // of itself): the first's rest is exact there (a multiple of y's last bit, at most 2^-4 of it), and
+          // so is its 28-fold.
+          auto terms = [&](int j, uint64_t y2, uint32_t(&p1)[q / 2], uint32_t(&p2)[q / 2]) {
+            const float2 y = unpack2(y2);
+            const __half2 h = __floats2half2_rn(y.x, y.y);
+            p1[j] = __nv_cvt_halfraw2_to_fp8x2(h, __NV_SATFINITE, __NV_E4M3);
+            const __half2_raw f = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)p1[j], __NV_E4M3);
+            p2[j] = __nv_cvt_halfraw2_to_fp8x2(__hmul2(__hsub2(h, __half2(f)), c28), __NV_SATFINITE, __NV_E4M3);
+          };
+          auto store = [&](uint8_t* d, const uint32_t(&p1)[q / 2], const uint32_t(&p2)[q / 2]) {
             if constexpr (q == 8) {
               *reinterpret_cast<uint4*>(d) = make_uint4(p1[0] | p1[1] << 16, p1[2] | p1[3] << 16, p2[0] | p2[1] << 16,
                                                         p2[2] | p2[3] << 16);
@@ -958,6 +970,56 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
               *reinterpret_cast<uint2*>(d) = make_uint2(p1[0] | p1[1] << 16, p2[0] | p2[1] << 16);
             } else {
               *reinterpret_cast<uint32_t*>(d) = p1[0] | p2[0] << 16;
+            }
+          };
+          if (es.x - es.y <= kSpread) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float cs = 448.f * c8_pow2(max(-126, ev[e] - es.x));
+              const uint64_t c2 = pack2(cs, cs);
+              uint32_t p1[q / 2], p2[q / 2];  // two codes each
+#pragma unroll
+              for (int j = 0; j < q / 2; ++j) {
+                const float2 x = unpack2(add2(z[e][j], mt[j]));
+                const uint64_t p = pack2(ex2_approx(x.x), ex2_approx(x.y));
+                ps[j] = add2(ps[j], p);
+                terms(j, mul2(p, c2), p1, p2);
+              }
+              store(pd + e * 128, p1, p2);
+            }
+          } else {
+            // The rows' own references: the largest score plus V exponent, rounded up. (A tile that comes here
+            // takes up to 25% longer with 32 rows, 1% with 8, where HBM binds; so it is not the only way.)
+            float mr[q];
+#pragma unroll
+            for (int j = 0; j < q; ++j) mr[j] = kNegMax;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+              for (int j = 0; j < q / 2; ++j) {
+                const float2 x = unpack2(add2(z[e][j], mt[j]));
+                mr[2 * j] = fmaxf(mr[2 * j], x.x + (float)ev[e]);
+                mr[2 * j + 1] = fmaxf(mr[2 * j + 1], x.y + (float)ev[e]);
+              }
+            const float own = across_tokens<q>(mr, lane, [](float x, float y) { return fmaxf(x, y); });
+            if ((lane >> 2) < q) sh.wref[wg][q4][row0 + (lane >> 2)] = own;
+            group_sync(1 + wg);
+            // (row t; the softmax warps' and the maxima's both read it behind another barrier)
+            if (t < NR)
+              sh.ref[wg][t] = ref_of(fmaxf(fmaxf(sh.wref[wg][0][t], sh.wref[wg][1][t]), fmaxf(sh.wref[wg][2][t], sh.wref[wg][3][t])));
+            group_sync(1 + wg);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t p1[q / 2], p2[q / 2];
+#pragma unroll
+              for (int j = 0; j < q / 2; ++j) {
+                const float2 x = unpack2(add2(z[e][j], mt[j]));
+                ps[j] = add2(ps[j], pack2(ex2_approx(x.x), ex2_approx(x.y)));
+                const float y0 = ex2_approx(x.x + (float)(ev[e] - sh.ref[wg][row0 + 2 * j]));
+                const float y1 = ex2_approx(x.y + (float)(ev[e] - sh.ref[wg][row0 + 2 * j + 1]));
+                terms(j, pack2(448.f * y0, 448.f * y1), p1, p2);
+              }
+              store(pd + e * 128, p1, p2);
             }
           }
           tc::fence_proxy_async();
@@ -1131,18 +1193,18 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache8_join_kernel(C8AttendAr
     const long slot = unit + c0 + p0 + lane * PER;
     const bool has = p0 + lane * PER < n;
     const float pm = has ? part.m(slot)[r] : kNegMax, pl = has ? part.l(slot)[r] : 0.f;
-    const int pe = has ? *part.e(slot) : -126;
+    const int pe = has ? part.e(slot)[r] : -126;
     // the sums so far and these pieces' on common references
     float mn = fmaxf(m, pm);
 #pragma unroll
     for (int h = 16; h; h >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, h));
-    const int en = max(e, __reduce_max_sync(0xFFFFFFFFu, pe));
+    const int en = max(ref_of(m - mn + (float)e), __reduce_max_sync(0xFFFFFFFFu, ref_of(pm - mn + (float)pe)));
     const float old = ex2_approx(m - mn), f = ex2_approx(pm - mn);
     float l = pl * f;
 #pragma unroll
     for (int h = 16; h; h >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, h);
     den = fmaf(den, old, l);
-    const float fe = f * c8_pow2(max(-126, pe - en)), olde = old * c8_pow2(max(-126, e - en));
+    const float fe = ex2_approx(pm - mn + (float)(pe - en)), olde = ex2_approx(m - mn + (float)(e - en));
 #pragma unroll
     for (int v = 0; v < kV; ++v) o[v] *= olde;
     m = mn;
@@ -1171,16 +1233,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache8_join_kernel(C8AttendAr
     for (int v = 0; v < kV; ++v) s_o[warp][lane * kV + v] = o[v];
     __syncthreads();  // (all warps of the CTA have the same item)
     if (warp > 0) return;
-    for (int x = 1; x < PER; ++x) {
-      m = fmaxf(m, s_m[x]);
-      e = max(e, s_e[x]);
-    }
+    for (int x = 1; x < PER; ++x) m = fmaxf(m, s_m[x]);
+    e = -126;
+    for (int x = 0; x < PER; ++x) e = max(e, ref_of(s_m[x] - m + (float)s_e[x]));
     den = 0.f;
 #pragma unroll
     for (int v = 0; v < kV; ++v) o[v] = 0.f;
 #pragma unroll
     for (int x = 0; x < PER; ++x) {
-      const float f = ex2_approx(s_m[x] - m), fe = f * c8_pow2(max(-126, s_e[x] - e));
+      const float f = ex2_approx(s_m[x] - m), fe = ex2_approx(s_m[x] - m + (float)(s_e[x] - e));
       den = fmaf(s_l[x], f, den);
 #pragma unroll
       for (int v = 0; v < kV; ++v) o[v] = fmaf(s_o[x][lane * kV + v], fe, o[v]);
@@ -1291,7 +1352,7 @@ cudaError_t launch_d(const C8AttendArgs& a, cudaStream_t s) {
 size_t cache8_part_bytes(int batch, int G, int rows, int d) {
   const Rows rw = rows_of(rows);
   const long units = (long)batch * G * rw.nch;
-  const long rec = (long)rw.nr * d + rw.nr * 2 + 4;
+  const long rec = (long)rw.nr * d + rw.nr * 3;
   return (size_t)(2 * ((units + 3) & ~3L) + (units + kGridMax) * rec) * 4;
 }
 

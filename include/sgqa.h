@@ -268,8 +268,10 @@ int sgqa_cache8_append(const sgqa_dims* dims, int block, const int32_t* lens, co
  * wrote (NULL: nothing yet; it may be weight_out itself).
  * A query with a NaN or an infinity gives NaN, itself and (visible tokens') weights; a NaN in V only the
  * dims and rows that see it. K and V are read from the codes as they are: q and the probabilities go to
- * the tensor cores as two E4M3 terms each (q exact but for elements below 2^-14 of their row's largest,
- * probabilities to 2^-8), scores, maxima, denominators and received weights are fp32.
+ * the tensor cores as two E4M3 terms each (q exact but for elements below 2^-14 of their row's largest;
+ * a token's probability times its V scale to 2^-8 of itself or, where that is less, to 2^-19 of the largest
+ * that its row has within the same 128 tokens, whatever other rows' or blocks' V may be), scores, maxima,
+ * denominators and received weights are fp32.
  * Requires n_new * Hq/G <= 64 (else SGQA_ERR_UNSUPPORTED). */
 int sgqa_cache8_attend(const sgqa_dims* dims, int block, const int32_t* lens, int n_new, const uint16_t* q,
                        const uint16_t* gate, const uint8_t* k8, const float* k_scale, const uint8_t* v8,
