@@ -8,6 +8,7 @@
 #include <cooperative_groups.h>
 
 #include "cache8.cuh"
+#include "clusters.h"
 
 namespace cg = cooperative_groups;
 
@@ -534,21 +535,18 @@ cudaError_t launch_keep(const C8EvictArgs& a, int ctas, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  if (ctas == 16) {
-    static const bool can = [&] {
-      int n = 0;
-      const bool ok = cudaFuncSetAttribute(cache8_keep_kernel<VEC, REG>, cudaFuncAttributeNonPortableClusterSizeAllowed,
-                                           1) == cudaSuccess &&
-                      cudaOccupancyMaxActiveClusters(&n, cache8_keep_kernel<VEC, REG>, &cfg) == cudaSuccess && n > 0;
-      if (!ok) (void)cudaGetLastError();
-      return ok;
-    }();
-    if (!can) {
-      at.val.clusterDim.x = 8;
-      cfg.gridDim = dim3((unsigned)(a.batch * a.G * 8));
-    }
+  const auto kernel = cache8_keep_kernel<VEC, REG>;
+  int most = 0;
+  const int n = cluster_ctas(
+      ctas,
+      [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess; },
+      [&] { return cudaOccupancyMaxActiveClusters(&most, kernel, &cfg) == cudaSuccess ? most : 0; });
+  if (n != ctas) {
+    (void)cudaGetLastError();
+    at.val.clusterDim.x = (unsigned)n;
+    cfg.gridDim = dim3((unsigned)(a.batch * a.G * n));
   }
-  return cudaLaunchKernelEx(&cfg, cache8_keep_kernel<VEC, REG>, a);
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 // Which selection: clusters of as few CTAs as hold a (sequence, group)'s weights in registers with eight
 // loads a lane, up to 8; of more while that leaves SMs without a CTA and a part 2048 weights or more.
