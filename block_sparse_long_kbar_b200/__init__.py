@@ -346,7 +346,8 @@ def sgqa_cache8_evict(dims, block, lens, keep, recent, T_out, weight, k8, k_scal
 
 
 def sgqa_test_stall_decode_cta(cta: int):
-    """Failure-detection test hook: decode attention CTA `cta` issues no loads (-1: off)."""
+    """Failure-detection test hook: decode attention CTA `cta` issues no loads (-1: off; from 2^20 on: CTA cta - 2^20
+    of sgqa_cache8_attend's pass for the received weights)."""
     _check("sgqa_test_stall_decode_cta", load_library().sgqa_test_stall_decode_cta(int(cta)))
 
 

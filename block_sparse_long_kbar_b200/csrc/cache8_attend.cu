@@ -596,7 +596,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
     const bool mine = j < per && !(W && part_v);
     int issued = 0, st = me;
     uint32_t ph = 1;
-    bool stop = !W && (int)blockIdx.x == a.stall_cta;
+    bool stop = (int)blockIdx.x == a.stall_cta - (W ? SGQA_TEST_STALL_WEIGHTS : 0);
     const uint64_t once = evict_first_policy();  // V where K is read again for the weights
     for (; w.left > 0 && !stop; walk_next<W>(w, a)) {
       const int src = (w.b * nblk + j) * a.G + w.g, z = w.b * a.T;
@@ -889,7 +889,9 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
           const float h0 = (up2 ? add[2] : add[0]) + __shfl_xor_sync(0xFFFFFFFFu, g0, 2);
           const float h1 = (up2 ? add[3] : add[1]) + __shfl_xor_sync(0xFFFFFFFFu, g1, 2);
           const float tot = (up1 ? h1 : h0) + __shfl_xor_sync(0xFFFFFFFFu, up1 ? h0 : h1, 1);
-          if (uw < w.L && !stopped) a.w_out[wi] = sum + tot;
+          // (after a wait of this CTA has run out the scores may be anything: the weight, which may be summed up
+          // in place, stays as it is)
+          if (uw < w.L && !stopped && !*abort) a.w_out[wi] = sum + tot;
         } else {
           // maxima of the tile; NaN counts for none (it reaches the sums by itself)
           float mx[q];

@@ -265,7 +265,8 @@ int sgqa_cache8_append(const sgqa_dims* dims, int block, const int32_t* lens, co
  * weight_out, if not NULL, [batch, G, T] fp32, receives for every token u < lens[b]
  *   (u < lens[b] - n_new ? weight_in[b,g,u] : 0) + sum over i and the heads of g of its probability,
  * the attention weight it has received so far, when weight_in [batch, G, T] is what the step before
- * wrote (NULL: nothing yet; it may be weight_out itself).
+ * wrote (NULL: nothing yet; it may be weight_out itself). After SGQA_ERR_TIMEOUT some of weight_out may
+ * be written and the rest as before: a call that adds up in place cannot be repeated then.
  * A query with a NaN or an infinity gives NaN, itself and (visible tokens') weights; a NaN in V only the
  * dims and rows that see it. K and V are read from the codes as they are: q and the probabilities go to
  * the tensor cores as two E4M3 terms each (q exact but for elements below 2^-14 of their row's largest;
@@ -295,12 +296,14 @@ int sgqa_cache8_evict(const sgqa_dims* dims, int block, const int32_t* lens, int
 
 /* Failure-detection test hook (host-side setting, not for production use). While cta >= 0, the
  * decode attention CTA with that grid index in later sgqa_decode / sgqa_decode_fp8 calls (and the
- * attention CTA in sgqa_cache8_attend) issues
+ * attention CTA in sgqa_cache8_attend; from SGQA_TEST_STALL_WEIGHTS on, the CTA cta -
+ * SGQA_TEST_STALL_WEIGHTS of its pass for the received weights) issues
  * no loads, so its tensor-core issuer's wait for the first tile is never satisfied: the wait
  * runs out after its bound (2 s), the kernel records SGQA_ERR_TIMEOUT in the status word and
  * returns with nothing in flight, and every other CTA and later kernel that polls that status
  * word stops early (until sgqa_reset_device_status). cta = -1 turns the hook off. Returns
  * SGQA_ERR_INVALID_ARG for cta < -1. Not thread-safe: set it while no other host thread calls. */
+#define SGQA_TEST_STALL_WEIGHTS (1 << 20)
 int sgqa_test_stall_decode_cta(int cta);
 
 /* Size of the library-owned scratch array that sgqa_decode_noalloc uses (16 MiB). */
