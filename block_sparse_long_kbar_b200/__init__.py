@@ -126,20 +126,46 @@ def _current_device():
     return _current_device()
 
 
-def _addresses(names, tensors):
-    """Addresses of contiguous tensors (None stays None), all on the current device; the last is ws."""
-    dev, out = tensors[-1].get_device(), []
-    for t in tensors:
+def _element_types():
+    """What a tensor of each kind may hold (bound on first use): bf16 rows, E4M3 codes, fp32, int32."""
+    global _element_types
+    import torch
+    kinds = {"h": (torch.bfloat16, torch.uint16, torch.int16), "c": (torch.uint8, torch.float8_e4m3fn, torch.int8),
+             "f": (torch.float32,), "i": (torch.int32,)}
+    _element_types = lambda: kinds
+    return kinds
+
+
+def _refuse(name, t, dev, kind, want, batch):
+    """Raises for what is wrong with a tensor; returns if that is only that it holds further sequences behind the batch's."""
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor on the device of ws")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.dtype not in kind:
+        raise ValueError(f"{name} must be of type {' or '.join(str(x) for x in kind)}, not {t.dtype}")
+    if t.dim() == 0 or t.shape[0] < batch or t.numel() * batch != want * t.shape[0]:
+        raise ValueError(f"{name} must have {want} elements, {want // batch} for each of {batch} sequences; its shape is {tuple(t.shape)}")
+
+
+def _addresses(names, kinds, tensors, ws, batch, counts):
+    """Addresses of contiguous tensors (None stays None) and of ws, all on the current device. counts: the elements
+    of each, or None where the library refuses the sizes by itself."""
+    dev, types, out = ws.get_device(), _element_types(), []
+    for t, k, n in zip(tensors, kinds, counts or (None,) * len(kinds)):
         if t is None:
             out.append(None)
-        elif t.get_device() != dev or dev < 0:
-            raise ValueError(f"{names.split()[len(out)]} must be a CUDA tensor on the device of ws")
-        elif not t.is_contiguous():
-            raise ValueError(f"{names.split()[len(out)]} must be contiguous")
-        else:
-            out.append(t.data_ptr())
+            continue
+        if n is None:
+            n = t.numel()
+        if t.numel() != n or t.dtype not in types[k] or t.get_device() != dev or not t.is_contiguous() or dev < 0:
+            _refuse(names.split()[len(out)], t, dev, types[k], n, batch)
+        out.append(t.data_ptr())
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
     if dev != _current_device():
         raise ValueError(f"the tensors are on device {dev}, not on the current one")
+    out.append(ws.data_ptr())
     return out
 
 
@@ -316,33 +342,55 @@ def sgqa_cache8_workspace_size(dims: sgqa_dims, block: int, n_new: int) -> int:
     return int(load_library().sgqa_cache8_workspace_size(ctypes.byref(dims), int(block), int(n_new)))
 
 
+_CACHE8_BLOCKS = (8, 16, 32, 64, 128)
+
+
 def sgqa_cache8_append(dims, block, lens, n_t, k_new, v_new, k8, k_scale, v8, v_scale, ws, counts=None, stream=None):
-    """Store the first counts[b] (default: all n_t) tokens of k_new, v_new behind the lens[b] cached ones."""
-    p = _addresses("lens counts k_new v_new k8 k_scale v8 v_scale ws",
-                   (lens, counts, k_new, v_new, k8, k_scale, v8, v_scale, ws))
+    """Store the first counts[b] (default: all n_t) tokens of k_new, v_new behind the lens[b] cached ones.
+    As in the two calls below, types and element counts have to be those of include/sgqa.h for these dims (more
+    sequences behind the batch's may be there); else ValueError."""
+    b, T, G, d, block, n_t = dims.batch, dims.T, dims.G, dims.d, int(block), int(n_t)
+    sizes = None
+    if block in _CACHE8_BLOCKS and min(b, T, G, d, n_t) > 0:
+        rows, new, scales = b * T * G * d, b * n_t * G * d, b * -(-T // block) * G
+        sizes = (b, b, new, new, rows, scales, rows, scales)
+    p = _addresses("lens counts k_new v_new k8 k_scale v8 v_scale", "iihhcfcf",
+                   (lens, counts, k_new, v_new, k8, k_scale, v8, v_scale), ws, b, sizes)
     _check("sgqa_cache8_append", load_library().sgqa_cache8_append(
-        ctypes.byref(dims), int(block), p[0], p[1], int(n_t), *p[2:], ws.numel(), _stream(stream)))
+        ctypes.byref(dims), block, p[0], p[1], n_t, *p[2:], ws.numel(), _stream(stream)))
 
 
 def sgqa_cache8_attend(dims, block, lens, n_new, q, gate, k8, k_scale, v8, v_scale, out, ws, weight_in=None,
                        weight_out=None, stream=None):
     """Dense gated attention of the last n_new of lens[b] tokens over the block-scaled 8-bit cache; with
     weight_out, also the attention weight that every token has received (on top of weight_in)."""
-    p = _addresses("lens q gate k8 k_scale v8 v_scale out weight_in weight_out ws",
-                   (lens, q, gate, k8, k_scale, v8, v_scale, out, weight_in, weight_out, ws))
+    b, T, G, d, block, n_new = dims.batch, dims.T, dims.G, dims.d, int(block), int(n_new)
+    sizes = None
+    if block in _CACHE8_BLOCKS and min(b, T, G, d, n_new, dims.Hq) > 0:
+        rows, new, scales, w = b * T * G * d, b * n_new * dims.Hq * d, b * -(-T // block) * G, b * G * T
+        sizes = (b, new, new, rows, scales, rows, scales, new, w, w)
+    p = _addresses("lens q gate k8 k_scale v8 v_scale out weight_in weight_out", "ihhcfcfhff",
+                   (lens, q, gate, k8, k_scale, v8, v_scale, out, weight_in, weight_out), ws, b, sizes)
     _check("sgqa_cache8_attend", load_library().sgqa_cache8_attend(
-        ctypes.byref(dims), int(block), p[0], int(n_new), *p[1:], ws.numel(), _stream(stream)))
+        ctypes.byref(dims), block, p[0], n_new, *p[1:], ws.numel(), _stream(stream)))
 
 
 def sgqa_cache8_evict(dims, block, lens, keep, recent, T_out, weight, k8, k_scale, v8, v_scale, k8_out, k_scale_out,
                       v8_out, v_scale_out, weight_out, kept, lens_out, ws, stream=None):
     """Move the `recent` last and the heaviest other tokens, `keep` in all per (sequence, group), to
     another cache of capacity T_out."""
-    p = _addresses("lens weight k8 k_scale v8 v_scale k8_out k_scale_out v8_out v_scale_out weight_out kept lens_out ws",
+    b, T, G, d, block, keep, T_out = dims.batch, dims.T, dims.G, dims.d, int(block), int(keep), int(T_out)
+    sizes = None
+    if block in _CACHE8_BLOCKS and min(b, T, G, d, keep, T_out) > 0:
+        bG, nb, nb_out = b * G, -(-T // block), -(-T_out // block)
+        sizes = (b, bG * T, bG * T * d, bG * nb, bG * T * d, bG * nb, bG * T_out * d, bG * nb_out, bG * T_out * d, bG * nb_out,
+                 bG * T_out, bG * keep, b)
+    p = _addresses("lens weight k8 k_scale v8 v_scale k8_out k_scale_out v8_out v_scale_out weight_out kept lens_out",
+                   "ifcfcfcfcffii",
                    (lens, weight, k8, k_scale, v8, v_scale, k8_out, k_scale_out, v8_out, v_scale_out, weight_out, kept,
-                    lens_out, ws))
+                    lens_out), ws, b, sizes)
     _check("sgqa_cache8_evict", load_library().sgqa_cache8_evict(
-        ctypes.byref(dims), int(block), p[0], int(keep), int(recent), int(T_out), *p[1:], ws.numel(), _stream(stream)))
+        ctypes.byref(dims), block, p[0], keep, int(recent), T_out, *p[1:], ws.numel(), _stream(stream)))
 
 
 def sgqa_test_stall_decode_cta(cta: int):
