@@ -45,6 +45,29 @@ bool cache_ok(const uint8_t* k8, const float* ks, const uint8_t* v8, const float
   return aligned16(k8) && aligned16(ks) && aligned16(v8) && aligned16(vs);
 }
 
+// Memory of a call's tensors: whether an output shares some with an input or another output.
+struct Span {
+  const void* p;
+  long bytes;
+};
+bool meet(const Span& x, const Span& y) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+  return x.p && y.p && a < b + (uintptr_t)y.bytes && b < a + (uintptr_t)x.bytes;
+}
+template <int IN, int OUT>
+bool overlap(const Span (&in)[IN], const Span (&out)[OUT]) {
+  for (int i = 0; i < OUT; ++i) {
+    for (const Span& x : in)
+      if (meet(x, out[i])) return true;
+    for (int j = 0; j < i; ++j)
+      if (meet(out[j], out[i])) return true;
+  }
+  return false;
+}
+// bytes of a cache's codes (K or V) and of their scales
+long code_bytes(const sgqa_dims* d, int T) { return (long)d->batch * T * d->G * d->d; }
+long scale_bytes(const sgqa_dims* d, int T, int block) { return (long)d->batch * (((long)T + block - 1) / block) * d->G * 4; }
+
 Cache8 cache_of(const uint8_t* k8, const float* ks, const uint8_t* v8, const float* vs) {
   return {const_cast<uint8_t*>(k8), const_cast<float*>(ks), const_cast<uint8_t*>(v8), const_cast<float*>(vs)};
 }
@@ -70,6 +93,10 @@ int sgqa_cache8_append(const sgqa_dims* dims, int block, const int32_t* lens, co
   if (n_t > 0 && (!aligned16(k_new) || !aligned16(v_new))) return SGQA_ERR_INVALID_ARG;
   if (!ws_ok(ws, ws_bytes, kStatusBytes)) return SGQA_ERR_WORKSPACE;
   if (n_t == 0) return SGQA_OK;
+  const long c = code_bytes(dims, dims->T), s = scale_bytes(dims, dims->T, block), x = code_bytes(dims, n_t) * 2;
+  if (overlap<4, 5>({{lens, dims->batch * 4L}, {counts, dims->batch * 4L}, {k_new, x}, {v_new, x}},
+                    {{k8, c}, {v8, c}, {k_scale, s}, {v_scale, s}, {ws, kStatusBytes}}))
+    return SGQA_ERR_INVALID_ARG;
   C8AppendArgs a{};
   a.lens = lens; a.counts = counts; a.k = k_new; a.v = v_new; a.c = cache_of(k8, k_scale, v8, v_scale);
   a.batch = dims->batch; a.T = dims->T; a.G = dims->G; a.d = dims->d; a.block = block; a.n_t = n_t;
@@ -91,6 +118,14 @@ int sgqa_cache8_attend(const sgqa_dims* dims, int block, const int32_t* lens, in
     return SGQA_ERR_INVALID_ARG;
   const Cache8Ws w = cache8_layout(dims, n_new, ws);
   if (!ws_ok(ws, ws_bytes, w.bytes)) return SGQA_ERR_WORKSPACE;
+  const long c = code_bytes(dims, dims->T), s = scale_bytes(dims, dims->T, block), x = (long)dims->batch * n_new * dims->Hq * dims->d * 2;
+  const long wt = (long)dims->batch * dims->G * dims->T * 4;
+  // (the gate of an element is read by the thread that writes it, and so is a weight's past: out may be gate,
+  // weight_out may be weight_in, whole)
+  if (overlap<8, 3>({{lens, dims->batch * 4L}, {q, x}, {k8, c}, {v8, c}, {k_scale, s}, {v_scale, s},
+                     {gate == out ? nullptr : gate, x}, {weight_in == weight_out ? nullptr : weight_in, wt}},
+                    {{out, x}, {weight_out, wt}, {ws, (long)w.bytes}}))
+    return SGQA_ERR_INVALID_ARG;
   C8AttendArgs a{};
   a.lens = lens; a.q = q; a.gate = gate; a.c = cache_of(k8, k_scale, v8, v_scale); a.out = out;
   a.w_in = weight_in; a.w_out = weight_out; a.lse = w.lse; a.part = w.part;
@@ -112,8 +147,13 @@ int sgqa_cache8_evict(const sgqa_dims* dims, int block, const int32_t* lens, int
       !cache_ok(k8_out, k_scale_out, v8_out, v_scale_out) || !aligned16(weight_out) || !aligned16(kept) ||
       !aligned16(lens_out))
     return SGQA_ERR_INVALID_ARG;
-  if (k8_out == k8 || v8_out == v8 || weight_out == weight || lens_out == lens) return SGQA_ERR_INVALID_ARG;
   if (!ws_ok(ws, ws_bytes, evict_bytes(dims))) return SGQA_ERR_WORKSPACE;
+  const long c = code_bytes(dims, dims->T), s = scale_bytes(dims, dims->T, block), w = (long)dims->batch * dims->G * dims->T * 4;
+  const long co = code_bytes(dims, T_out), so = scale_bytes(dims, T_out, block), n = (long)dims->batch * dims->G * 4;
+  if (overlap<6, 8>({{lens, dims->batch * 4L}, {weight, w}, {k8, c}, {v8, c}, {k_scale, s}, {v_scale, s}},
+                    {{k8_out, co}, {v8_out, co}, {k_scale_out, so}, {v_scale_out, so}, {weight_out, n * T_out},
+                     {kept, n * keep}, {lens_out, dims->batch * 4L}, {ws, (long)evict_bytes(dims)}}))
+    return SGQA_ERR_INVALID_ARG;
   C8EvictArgs a{};
   a.grid_ws = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + kStatusBytes);
   a.lens = lens; a.weight = weight; a.src = cache_of(k8, k_scale, v8, v_scale);

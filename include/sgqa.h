@@ -240,7 +240,8 @@ int sgqa_gated_swa(const sgqa_dims* dims, int window, const uint16_t* q, const u
  * The lengths are read on the device when the call runs, so that one captured graph serves every
  * length. One that does not fit (negative, or beyond the capacity) is recorded as
  * SGQA_ERR_DEVICE_CHECK and its sequence is skipped (append) or taken as empty (attend, evict).
- * Of dims, d_idx, B and k are checked like everywhere but not used.
+ * Of dims, d_idx, B and k are checked like everywhere but not used. An output that shares memory with an
+ * input, another output or the workspace is refused (SGQA_ERR_INVALID_ARG), except where a call says so.
  *
  * Bytes of workspace that any of the three calls below needs, n_new being the most tokens a step of
  * sgqa_cache8_attend has; 0 if invalid or unsupported. */
@@ -261,7 +262,7 @@ int sgqa_cache8_append(const sgqa_dims* dims, int block, const int32_t* lens, co
  * whole cache: with p_i = lens[b] - n_new + i the position of query i, head h of group g and x = code *
  * scale,  o = softmax_{u <= p_i}(q[b,i,h] . k[b,u,g] / sqrt(d)) v;  out[b,i,h,:] = o *
  * sigmoid(gate[b,i,h,:]).  q, gate, out [batch, n_new, Hq, d] bf16. Rows without a position (p_i < 0)
- * get zeros.
+ * get zeros. out may be gate.
  * weight_out, if not NULL, [batch, G, T] fp32, receives for every token u < lens[b]
  *   (u < lens[b] - n_new ? weight_in[b,g,u] : 0) + sum over i and the heads of g of its probability,
  * the attention weight it has received so far, when weight_in [batch, G, T] is what the step before
@@ -287,7 +288,7 @@ int sgqa_cache8_attend(const sgqa_dims* dims, int block, const int32_t* lens, in
  * take the scale of their new block; a row whose scale does not change keeps its bits. Writes
  *   kept [batch, G, keep] int32, the positions that stay, ascending, then -1;
  *   lens_out [batch] int32 = min(lens[b], keep);  weight_out [batch, G, T_out], the weights that stay.
- * No output may overlap an input. batch * T_out * G < 2^31 (else SGQA_ERR_UNSUPPORTED). */
+ * batch * T_out * G < 2^31 (else SGQA_ERR_UNSUPPORTED). */
 int sgqa_cache8_evict(const sgqa_dims* dims, int block, const int32_t* lens, int keep, int recent, int T_out,
                       const float* weight, const uint8_t* k8, const float* k_scale, const uint8_t* v8,
                       const float* v_scale, uint8_t* k8_out, float* k_scale_out, uint8_t* v8_out,
