@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kThr) cache8_append_kernel(C8AppendArgs a, int
   int item = first + sub, j = j0 + item / a.G, g = item % a.G;
   for (int it = 0; it < loop; ++it) {
     const int u0 = j * BLK;
-    const bool live = item < items && u0 < end;
+    const bool live = item < items && u0 < end && SGQA_CHECK(j < nblk && g < a.G, a.status);
     uint4 xk[kPass][2], xv[kPass][2];
     uint32_t mk = 0, mv = 0;
 #pragma unroll
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kThr) cache8_append_kernel(C8AppendArgs a, int
 #pragma unroll
       for (int p = 0; p < kPass; ++p) {
         const int u = u0 + row0 + p * kRows;
-        if (u >= end) break;
+        if (u >= end || !SGQA_CHECK(u < a.T, a.status)) break;
         const long dst = (long)((b * a.T + u) * a.G + g) * D + col;
         uint4* ok = reinterpret_cast<uint4*>(a.c.k8 + dst);
         uint4* ov = reinterpret_cast<uint4*>(a.c.v8 + dst);

@@ -452,7 +452,7 @@ __device__ __forceinline__ void split_q(const C8AttendArgs& a, const Walk& w, Sh
     const int gr = r0 + r, i = gr / R;
     uint4 x[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
     float lse = INFINITY;  // no row: 2^-inf
-    if (r < real) {
+    if (r < real && SGQA_CHECK(w.b < a.batch && w.g < a.G && gr < rows, a.status)) {
       const uint4* src = reinterpret_cast<const uint4*>(
           a.q + (((long)w.b * a.n_new + i) * a.Hq + (long)w.g * R + gr - i * R) * D + chunk * 16);
       x[0] = __ldg(src);
@@ -602,6 +602,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
       const int src = (w.b * nblk + j) * a.G + w.g, z = w.b * a.T;
       for (int x = (me + C::kFetch - w.k % C::kFetch) % C::kFetch; x < w.t1 - w.t0; x += C::kFetch) {
         const int tile = walk_tile<W>(w, x);
+        // (a tile that is none reads zeros or another's rows)
+        const bool in = SGQA_CHECK(w.b < a.batch && w.g < a.G && tile >= 0 && tile * kTok < w.L, a.status);
         if (w.k + x >= C::kStages) {
           warp_wait(&sh.empty[st], ph, abort, a.status);
           if ((stop = __any_sync(0xFFFFFFFFu, *abort))) break;
@@ -618,7 +620,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
           }
         }
         const int blk = tile * per;
-        if (mine && blk + j < nblk) cp_async4(&sh.scale[st][lane], scales + (src + blk * a.G));
+        if (mine && in && blk + j < nblk) cp_async4(&sh.scale[st][lane], scales + (src + blk * a.G));
         cp_async_arrive(&sh.full[st]);
         issued = w.k + x + 1;
         st += C::kFetch;
@@ -754,7 +756,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
           }
         }
         const long slot = (long)w.b * units_b + w.g * a.nch + w.ch + blockIdx.x;
-        if (lane < NR) {
+        if (lane < NR && SGQA_CHECK(slot < (long)a.batch * units_b + kGridMax, a.status)) {
           part.m(slot)[lane] = m_run;
           part.l(slot)[lane] = l;
           part.e(slot)[lane] = e_run;
@@ -794,7 +796,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
         const long wi = wi0 + uw;
         float sum = 0.f;
         if constexpr (W) {
-          if (a.w_in && uw < vis) sum = a.w_in[wi];
+          if (a.w_in && uw < vis && SGQA_CHECK(w.b < a.batch && uw >= 0 && uw < a.T, a.status)) sum = a.w_in[wi];
         }
         warp_wait(&sh.s_full[wg], kp & 1u, abort, a.status);
         warp_wait(&sh.full[st], ph, abort, a.status);
@@ -891,7 +893,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
           const float tot = (up1 ? h1 : h0) + __shfl_xor_sync(0xFFFFFFFFu, up1 ? h0 : h1, 1);
           // (after a wait of this CTA has run out the scores may be anything: the weight, which may be summed up
           // in place, stays as it is)
-          if (uw < w.L && !stopped && !*abort) a.w_out[wi] = sum + tot;
+          if (uw < w.L && !stopped && !*abort && SGQA_CHECK(w.b < a.batch && uw >= 0 && uw < a.T, a.status))
+            a.w_out[wi] = sum + tot;
         } else {
           // maxima of the tile; NaN counts for none (it reaches the sums by itself)
           float mx[q];
@@ -1119,14 +1122,16 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
           }
         }
         float* po = part.o(slot) + rb * D + dim;
+        const bool in = SGQA_CHECK(unit < (long)a.batch * units_b && slot < (long)a.batch * units_b + kGridMax, a.status);
 #pragma unroll
         for (int r = 0; r < C::kRowsT; r += 2) {
+          if (!in) break;
           const float2 y = unpack2(o[r / 2]);
           po[r * D] = y.x;
           po[(r + 1) * D] = y.y;
           o[r / 2] = 0ull;
         }
-        if (t == 0) {
+        if (t == 0 && in) {
           if (w.t0 == 0) part.first[unit] = (int)blockIdx.x;
           if (w.t1 == w.ntiles) part.last[unit] = (int)blockIdx.x;
         }
@@ -1186,6 +1191,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache8_join_kernel(C8AttendAr
     c0 = part.first[unit];
     c1 = part.last[unit];
   }
+  if (!SGQA_CHECK(!some || (c0 >= 0 && c0 <= c1 && c1 < a.main_ctas), a.status)) c0 = 0, c1 = -1;
   const int n = c1 - c0 + 1;  // pieces; this warp's are part_of, part_of + PER, ..
   float m = kNegMax, den = 0.f, o[kV];
   int e = -126;

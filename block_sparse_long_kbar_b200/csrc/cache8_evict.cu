@@ -127,8 +127,8 @@ struct Part {
   // ng0 heavier ones and ne0 equals precede these vectors. A lane's counts in two vectors, heavier and
   // equal, are four bytes of a word (a warp has at most 128 of each), so that one scan over the lanes
   // serves both.
-  __device__ __forceinline__ void emit(int base, uint32_t thr, uint32_t ties, uint32_t ng0, uint32_t ne0, int32_t* kept,
-                                       uint32_t* ng_out = nullptr, uint32_t* ne_out = nullptr) const {
+  __device__ __forceinline__ void emit(const C8EvictArgs& a, int base, uint32_t thr, uint32_t ties, uint32_t ng0,
+                                       uint32_t ne0, int32_t* kept, uint32_t* ng_out = nullptr, uint32_t* ne_out = nullptr) const {
     const int lane = threadIdx.x & 31;
     uint32_t ng = ng0, ne = ne0;
 #pragma unroll
@@ -156,7 +156,9 @@ struct Part {
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const bool is_gt = key[s][x] > thr, is_eq = key[s][x] == thr;
-          if (is_gt || (is_eq && pe < ties)) kept[pg + min(pe, ties)] = 4 * (base + s * 32 + lane) - off + x;
+          if ((is_gt || (is_eq && pe < ties)) &&
+              SGQA_CHECK(pg + min(pe, ties) < (uint32_t)(a.keep - a.recent), a.status))
+            kept[pg + min(pe, ties)] = 4 * (base + s * 32 + lane) - off + x;
           pg += is_gt ? 1u : 0u;
           pe += is_eq ? 1u : 0u;
         }
@@ -280,7 +282,7 @@ __global__ void __launch_bounds__(kSelThr) cache8_keep_kernel(C8EvictArgs a) {
     ne += x[1];
   }
   int32_t* kept = a.kept + (long)unit * a.keep;
-  pass_over([&](int base) { part.emit(base, prefix, need, ng, ne, kept, &ng, &ne); });
+  pass_over([&](int base) { part.emit(a, base, prefix, need, ng, ne, kept, &ng, &ne); });
   cluster.sync();  // no CTA leaves while another reads its shared memory
 }
 
@@ -354,7 +356,7 @@ __global__ void __launch_bounds__(kGridThr, 2) cache8_keep_grid_kernel(C8EvictAr
       }
       block_scan(bg, buf, &before_g);
       block_scan(be, buf, &before_e);
-      part.emit(part.v0, prefix, need, ng + before_g, ne + before_e, a.kept + (long)unit * a.keep);
+      part.emit(a, part.v0, prefix, need, ng + before_g, ne + before_e, a.kept + (long)unit * a.keep);
     }
   }
 }
@@ -413,7 +415,8 @@ __global__ void __launch_bounds__(kThr, BLK * D == 128 * 128 ? 4 : 0) cache8_mov
       const int i = x.j * BLK + row0 + p * kRows;
       // (a plain load: written by the kernel before, whose end is waited for in this one)
       x.u[p] = there && i < m ? a.kept[(long)(b * a.G + x.g) * a.keep + i] : -1;
-      if (!SGQA_CHECK(x.u[p] < a.T, a.status)) x.u[p] = -1;
+      if (!SGQA_CHECK(!(there && i < m) || (x.u[p] >= 0 && x.u[p] < a.T && i < a.T_out && x.j < nblk_out), a.status))
+        x.u[p] = -1;
     }
   };
   auto step = [&](Item& x) {
