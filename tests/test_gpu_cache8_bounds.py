@@ -164,3 +164,19 @@ def test_blocks_of_many_sizes(d, R, n):
         for j in range(s["vs"].shape[1]):
             s["vs"][:, j] *= 2.0 ** (spread * (j * 7 % 5 - 2))
         check(s, block, lens, q, gate)
+
+
+def test_alone_and_in_a_batch():
+    """A sequence by itself and among others: the same within both calls' bounds (bits may differ, since the
+    tiles of all sequences are cut into equal pieces)."""
+    gen = torch.Generator().manual_seed(14)
+    lens, G, d, block, T = [3000, 17, 901, 1400], 2, 128, 64, 3001
+    c = c8.to_cuda(c8.filled_cache(gen, lens, T, G, d, block))
+    q, gate = queries(gen, 4, 2, 16, d)
+    got, _, tol = check(c, block, lens, q, gate)
+    for b, L in enumerate(lens):
+        one = {n: t[b:b + 1].clone() for n, t in c.items()}
+        alone = attend(one, block, [L], q[b:b + 1].clone(), gate[b:b + 1].clone())
+        assert bool(((alone.double() - got[b:b + 1].double()).abs() <= 2 * tol[b:b + 1]).all())
+        again = attend(one, block, [L], q[b:b + 1].clone(), gate[b:b + 1].clone())
+        assert torch.equal(alone, again)
