@@ -273,7 +273,7 @@ int sgqa_cache8_append(const sgqa_dims* dims, int block, const int32_t* lens, co
  * the tensor cores as two E4M3 terms each (q exact but for elements below 2^-14 of their row's largest;
  * a token's probability times its V scale to 2^-8 of itself or, where that is less, to 2^-19 of the largest
  * that its row has within the same 128 tokens, whatever other rows' or blocks' V may be), scores, maxima,
- * denominators and received weights are fp32. A call repeats bit for bit; in another batch a sequence's
+ * denominators and received weights are fp32, and queries of 2^112 or more can give NaN. A call repeats bit for bit; in another batch a sequence's
  * results may differ within these bounds, since the work of all sequences is cut into equal pieces.
  * Requires n_new * Hq/G <= 64 (else SGQA_ERR_UNSUPPORTED). */
 int sgqa_cache8_attend(const sgqa_dims* dims, int block, const int32_t* lens, int n_new, const uint16_t* q,

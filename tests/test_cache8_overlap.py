@@ -90,3 +90,9 @@ def test_out_over_gate_and_weights_in_place():
         for bad in (q, k8.view(torch.bfloat16).flatten()[:q.numel()] if k8.numel() >= 2 * q.numel() else q):
             with pytest.raises(sg.SgqaError):
                 sg.sgqa_cache8_attend(dm, 16, lens, n, q, gate, k8, ks, v8, ks, bad, ws)
+
+
+@pytest.mark.parametrize("R,d", [(1, 64), (3, 128), (8, 128), (11, 64), (16, 128)])
+def test_a_workspace_for_more_new_tokens_holds_fewer(lib, R, d):
+    sizes = [sg.sgqa_cache8_workspace_size(sg.sgqa_dims(3, 4000, 4 * R, 4, d, 32, 8, 512), 16, n) for n in range(1, 64 // R + 1)]
+    assert sizes == sorted(sizes) and sizes[0] > 0
