@@ -126,47 +126,49 @@ def _current_device():
     return _current_device()
 
 
-def _element_types():
-    """What a tensor of each kind may hold (bound on first use): bf16 rows, E4M3 codes, fp32, int32."""
+def _element_types(kinds):
+    """What tensors of these kinds hold (bound on first use): h bf16 rows, c E4M3 codes, f fp32, i int32."""
     global _element_types
     import torch
-    kinds = {"h": (torch.bfloat16, torch.uint16, torch.int16), "c": (torch.uint8, torch.float8_e4m3fn, torch.int8),
-             "f": (torch.float32,), "i": (torch.int32,)}
-    _element_types = lambda: kinds
-    return kinds
+    of = {"h": torch.bfloat16, "c": torch.uint8, "f": torch.float32, "i": torch.int32}
+    table = {k: tuple(of[x] for x in k) for k in ("iihhcfcf", "ihhcfcfhff", "ifcfcfcfcffii")}
+    _element_types = table.__getitem__
+    return table[kinds]
 
 
-def _refuse(name, t, dev, kind, want, batch):
-    """Raises for what is wrong with a tensor; returns if that is only that it holds further sequences behind the batch's."""
+def _other(name, t, dev, dtype, want, batch):
+    """Raises for what is wrong with a tensor; returns if it only has another type for the same bits, or further
+    sequences behind the batch's."""
+    import torch
     if t.get_device() != dev or dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor on the device of ws")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.dtype not in kind:
-        raise ValueError(f"{name} must be of type {' or '.join(str(x) for x in kind)}, not {t.dtype}")
-    if t.dim() == 0 or t.shape[0] < batch or t.numel() * batch != want * t.shape[0]:
+    bits = {torch.bfloat16: (torch.uint16, torch.int16), torch.uint8: (torch.float8_e4m3fn, torch.int8)}.get(dtype, ())
+    if t.dtype is not dtype and t.dtype not in bits:
+        raise ValueError(f"{name} must be of type {' or '.join(str(x) for x in (dtype, *bits))}, not {t.dtype}")
+    if want is not None and (t.dim() == 0 or t.shape[0] < batch or t.numel() * batch != want * t.shape[0]):
         raise ValueError(f"{name} must have {want} elements, {want // batch} for each of {batch} sequences; its shape is {tuple(t.shape)}")
 
 
 def _addresses(names, kinds, tensors, ws, batch, counts):
-    """Addresses of contiguous tensors (None stays None) and of ws, all on the current device. counts: the elements
-    of each, or None where the library refuses the sizes by itself."""
-    dev, types, out = ws.get_device(), _element_types(), []
-    for t, k, n in zip(tensors, kinds, counts or (None,) * len(kinds)):
+    """Addresses of contiguous tensors (None stays None) and of ws, all on the current device, which is returned
+    too. counts: the elements of each, or None where the library refuses the sizes by itself. (One line of checks a
+    tensor: it is a good part of what a small call takes on the host.)"""
+    dev, out = ws.get_device(), []
+    for t, dtype, n in zip(tensors, _element_types(kinds), counts or (None,) * len(kinds)):
         if t is None:
             out.append(None)
             continue
-        if n is None:
-            n = t.numel()
-        if t.numel() != n or t.dtype not in types[k] or t.get_device() != dev or not t.is_contiguous() or dev < 0:
-            _refuse(names.split()[len(out)], t, dev, types[k], n, batch)
+        if t.numel() != n or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+            _other(names.split()[len(out)], t, dev, dtype, n, batch)
         out.append(t.data_ptr())
-    if not ws.is_contiguous():
-        raise ValueError("ws must be contiguous")
+    if dev < 0 or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous CUDA tensor")
     if dev != _current_device():
         raise ValueError(f"the tensors are on device {dev}, not on the current one")
     out.append(ws.data_ptr())
-    return out
+    return dev, out
 
 
 def _current_stream(device):
@@ -178,9 +180,9 @@ def _current_stream(device):
     return _current_stream(device)
 
 
-def _stream(stream):
+def _stream(stream, device=None):
     if stream is None:
-        return _current_stream(_current_device())
+        return _current_stream(_current_device() if device is None else device)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -351,28 +353,28 @@ def sgqa_cache8_append(dims, block, lens, n_t, k_new, v_new, k8, k_scale, v8, v_
     sequences behind the batch's may be there); else ValueError."""
     b, T, G, d, block, n_t = dims.batch, dims.T, dims.G, dims.d, int(block), int(n_t)
     sizes = None
-    if block in _CACHE8_BLOCKS and min(b, T, G, d, n_t) > 0:
+    if block in _CACHE8_BLOCKS and b > 0 and T > 0 and G > 0 and d > 0 and n_t > 0:
         rows, new, scales = b * T * G * d, b * n_t * G * d, b * -(-T // block) * G
         sizes = (b, b, new, new, rows, scales, rows, scales)
-    p = _addresses("lens counts k_new v_new k8 k_scale v8 v_scale", "iihhcfcf",
-                   (lens, counts, k_new, v_new, k8, k_scale, v8, v_scale), ws, b, sizes)
+    dev, p = _addresses("lens counts k_new v_new k8 k_scale v8 v_scale", "iihhcfcf",
+                        (lens, counts, k_new, v_new, k8, k_scale, v8, v_scale), ws, b, sizes)
     _check("sgqa_cache8_append", load_library().sgqa_cache8_append(
-        ctypes.byref(dims), block, p[0], p[1], n_t, *p[2:], ws.numel(), _stream(stream)))
+        ctypes.byref(dims), block, p[0], p[1], n_t, *p[2:], ws.numel(), _stream(stream, dev)))
 
 
 def sgqa_cache8_attend(dims, block, lens, n_new, q, gate, k8, k_scale, v8, v_scale, out, ws, weight_in=None,
                        weight_out=None, stream=None):
     """Dense gated attention of the last n_new of lens[b] tokens over the block-scaled 8-bit cache; with
     weight_out, also the attention weight that every token has received (on top of weight_in)."""
-    b, T, G, d, block, n_new = dims.batch, dims.T, dims.G, dims.d, int(block), int(n_new)
+    b, T, Hq, G, d, block, n_new = dims.batch, dims.T, dims.Hq, dims.G, dims.d, int(block), int(n_new)
     sizes = None
-    if block in _CACHE8_BLOCKS and min(b, T, G, d, n_new, dims.Hq) > 0:
-        rows, new, scales, w = b * T * G * d, b * n_new * dims.Hq * d, b * -(-T // block) * G, b * G * T
+    if block in _CACHE8_BLOCKS and b > 0 and T > 0 and G > 0 and d > 0 and n_new > 0 and Hq > 0:
+        rows, new, scales, w = b * T * G * d, b * n_new * Hq * d, b * -(-T // block) * G, b * G * T
         sizes = (b, new, new, rows, scales, rows, scales, new, w, w)
-    p = _addresses("lens q gate k8 k_scale v8 v_scale out weight_in weight_out", "ihhcfcfhff",
-                   (lens, q, gate, k8, k_scale, v8, v_scale, out, weight_in, weight_out), ws, b, sizes)
+    dev, p = _addresses("lens q gate k8 k_scale v8 v_scale out weight_in weight_out", "ihhcfcfhff",
+                        (lens, q, gate, k8, k_scale, v8, v_scale, out, weight_in, weight_out), ws, b, sizes)
     _check("sgqa_cache8_attend", load_library().sgqa_cache8_attend(
-        ctypes.byref(dims), block, p[0], n_new, *p[1:], ws.numel(), _stream(stream)))
+        ctypes.byref(dims), block, p[0], n_new, *p[1:], ws.numel(), _stream(stream, dev)))
 
 
 def sgqa_cache8_evict(dims, block, lens, keep, recent, T_out, weight, k8, k_scale, v8, v_scale, k8_out, k_scale_out,
@@ -381,16 +383,16 @@ def sgqa_cache8_evict(dims, block, lens, keep, recent, T_out, weight, k8, k_scal
     another cache of capacity T_out."""
     b, T, G, d, block, keep, T_out = dims.batch, dims.T, dims.G, dims.d, int(block), int(keep), int(T_out)
     sizes = None
-    if block in _CACHE8_BLOCKS and min(b, T, G, d, keep, T_out) > 0:
+    if block in _CACHE8_BLOCKS and b > 0 and T > 0 and G > 0 and d > 0 and keep > 0 and T_out > 0:
         bG, nb, nb_out = b * G, -(-T // block), -(-T_out // block)
         sizes = (b, bG * T, bG * T * d, bG * nb, bG * T * d, bG * nb, bG * T_out * d, bG * nb_out, bG * T_out * d, bG * nb_out,
                  bG * T_out, bG * keep, b)
-    p = _addresses("lens weight k8 k_scale v8 v_scale k8_out k_scale_out v8_out v_scale_out weight_out kept lens_out",
-                   "ifcfcfcfcffii",
-                   (lens, weight, k8, k_scale, v8, v_scale, k8_out, k_scale_out, v8_out, v_scale_out, weight_out, kept,
-                    lens_out), ws, b, sizes)
+    dev, p = _addresses("lens weight k8 k_scale v8 v_scale k8_out k_scale_out v8_out v_scale_out weight_out kept lens_out",
+                        "ifcfcfcfcffii",
+                        (lens, weight, k8, k_scale, v8, v_scale, k8_out, k_scale_out, v8_out, v_scale_out, weight_out, kept,
+                         lens_out), ws, b, sizes)
     _check("sgqa_cache8_evict", load_library().sgqa_cache8_evict(
-        ctypes.byref(dims), block, p[0], keep, int(recent), T_out, *p[1:], ws.numel(), _stream(stream)))
+        ctypes.byref(dims), block, p[0], keep, int(recent), T_out, *p[1:], ws.numel(), _stream(stream, dev)))
 
 
 def sgqa_test_stall_decode_cta(cta: int):
