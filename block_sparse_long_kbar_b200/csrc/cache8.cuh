@@ -5,8 +5,8 @@
 // and KV group, [batch, ceil(T / block), G] fp32: s = 2^e with e the smallest integer of [-126, 119]
 // such that max |x| <= 448 s over the block's finite values (448: E4M3's largest value; at 119 code
 // times scale stays finite); a code is x / s rounded to nearest even, saturating; NaN stays NaN and
-// counts for no scale. A power of two makes the value code * s exact in bf16 and fp32, and moving a row to a block of another scale
-// loses nothing but what falls below that block's subnormal step.
+// counts for no scale. A power of two makes the value code * s exact in bf16 and fp32, and moving a row to
+// a block of another scale loses nothing but what falls below that block's subnormal step.
 #pragma once
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -115,8 +115,8 @@ __device__ __forceinline__ uint32_t c8_rescale4(uint32_t w, float f) {
   const float2 a = c8_decode2(w), b = c8_decode2(w >> 16);
   return c8_encode2(a.x * f, a.y * f) | (c8_encode2(b.x * f, b.y * f) << 16);
 }
-// 16 codes times 2^k, rounded to E4M3 again. For k of [-24, 15] in fp16: a product of 2^-11 or more is
-// exact there, one below becomes 0 as it should.
+// two codes times 2^k, rounded to E4M3 again, for k of [-24, 15] in fp16: a product of 2^-11 or more is exact there,
+// one below becomes 0 as it should.
 __device__ __forceinline__ uint32_t c8_rescale2_half(uint32_t two, __half2 f) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(two & 0xFFFFu), __NV_E4M3);
   const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h), f);
@@ -125,6 +125,7 @@ __device__ __forceinline__ uint32_t c8_rescale2_half(uint32_t two, __half2 f) {
 // 2^k for rescaling codes; beyond +-40 every code but 0 saturates or vanishes anyway
 __device__ __forceinline__ float c8_shift(int k) { return c8_pow2(max(-40, min(40, k))); }
 
+// 16 codes times 2^k, rounded to E4M3 again
 __device__ __forceinline__ uint4 c8_rescale16(const uint4& x, int k) {
   if (k == 0) return x;
   if (k > 15) {

@@ -33,12 +33,13 @@
 // the last tile to the first, so that it finds in L2 what the first pass has read last.
 //
 // Measured (B200, inputs changing from pass to pass): 32 sequences of up to 32K tokens, 8 rows a group
-// (762 MB): 126 us a call, the first kernel 118 us = 6.5 TB/s, at the rate of a copy. 1M tokens, 4
-// groups of 32 rows (1.07 GB): 195 us a call on a cool GPU, 235 us in a long run, where the SM clock
-// falls to 1.67 GHz under the power cap (4.5 TB/s): the 32 rows take 1100 to 1250 cycles a tile, the
-// accumulating warps first. With weights, 8 sequences of 64K (454 MB and K again): 117 us, of which 70
-// the first kernel and 32 the pass over K, a third of it from L2. Small calls are launches, one chain of
-// cold loads and instruction fetch: 8 us on the device for 1900 tokens.
+// (762 MB): 128 us a call, 121 on the device, at 97% of a copy's rate. 1M tokens, 4 groups of 32 rows
+// (1.07 GB): 194 us on the device on a cool GPU, 240 us a call in a long run, where the SM clock falls to
+// 1.67 GHz under the power cap (4.5 TB/s): the 32 rows take 1100 to 1250 cycles a tile, the accumulating
+// warps first (96 registers for every role, with 92 bytes spilled at d 128). With weights, 8 sequences of
+// 64K (454 MB and K again): 118 us, of which 70 the first kernel and 32 the pass over K, a third of it from
+// L2. Small calls are launches, one chain of cold loads and instruction fetch: 8 us on the device for 1900
+// tokens. More than 32 rows make two units, which read K and V once each.
 // Not taken: two terms added up in one column of S^T or O^T (the second would need its scale inside the
 // MMA), a maximum carried over from earlier tiles (loses the digits above), converting to fp16 (0.4
 // us of a tile's 0.75 for the conversions alone, and twice the shared memory).
@@ -907,7 +908,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, W>::kThreads, 1)
           const float mine = across_tokens<q>(mx, lane, [](float x, float y) { return fmaxf(x, y); });
           we = __reduce_max_sync(0xFFFFFFFFu, we);
           wl = __reduce_min_sync(0xFFFFFFFFu, wl);
-          // the P buffer and the numbers of the tile two tiles back have been read
+          // the P buffer and the numbers of the group's tile before have been read
           if (kp > 0) warp_wait(&sh.o_empty[wg], (kp & 1u) ^ 1u, abort, a.status);
           if ((lane >> 2) < q) sh.wmax[wg][q4][row0 + (lane >> 2)] = mine;
           if (lane == 0) sh.wev[wg][q4] = make_int2(we, wl);
@@ -1281,7 +1282,7 @@ EncodeTiled get_encode() {
   return fn;
 }
 // [batch * T tokens][G][d] codes, box = one group's codes of 128 tokens; zeros behind the last token.
-// (With promotion to 256 bytes L2 fetched the neighbouring group along: 5.0 instead of 7.0 TB/s.)
+// (With promotion to 256 bytes L2 fetches the neighbouring group along: 32 x 32K 164 us on the device instead of 121.)
 bool make_map(CUtensorMap* map, const void* base, long tokens, int G, int d) {
   EncodeTiled enc = get_encode();
   if (!enc) return false;

@@ -380,8 +380,8 @@ __device__ __forceinline__ uint32_t amax16(const uint4& x, float scale) {
   return __float_as_uint(c8_decode2(m).x * scale);
 }
 // One item per block of the new cache and group, rows and items as in the append kernel. HBM bound: a
-// kept row is read and written once (with streaming stores: 59 us a call instead of 63 for 32 sequences of
-// 8K, of which the write-back of ordinary ones took the difference).
+// kept row is read and written once (with streaming stores 32 sequences of 8K take 59 us on the device instead of
+// 63, of which the write-back of ordinary ones took the difference).
 constexpr int kLoop = 8;
 template <int D, int BLK>
 __global__ void __launch_bounds__(kThr, BLK * D == 128 * 128 ? 4 : 0) cache8_move_kernel(C8EvictArgs a, int loop) {
